@@ -24,6 +24,8 @@ MOE_ERR_HIP = -2
 ERRBIT_BAD_ID = 1
 ERRBIT_RANK_CAP = 2
 ERRBIT_EXPERT_CAP = 4
+ERRBIT_BAD_LOGIT = 8
+ERRBIT_BAD_SEQ = 16
 
 EXPORTS = ("moe_abi_version", "moe_status_string", "moe_dispatch_layout",
            "moe_dispatch_layout_noalloc", "moe_layout_workspace_bytes", "moe_dispatch_pack",
@@ -31,7 +33,9 @@ EXPORTS = ("moe_abi_version", "moe_status_string", "moe_dispatch_layout",
            "moe_combine_ranks", "moe_dispatch_pack_mxfp8", "moe_permute_by_expert_mxfp8",
            "moe_dispatch_pack_mxfp4", "moe_permute_by_expert_mxfp4",
            "moe_dispatch_pack_nvfp4", "moe_permute_by_expert_nvfp4",
-           "moe_dispatch", "moe_dispatch_quantised", "moe_testing_set_layout_form",
+           "moe_dispatch", "moe_dispatch_quantised", "moe_route", "moe_route_backward",
+           "moe_balance_loss", "moe_balance_workspace_bytes", "moe_expert_product",
+           "moe_testing_set_layout_form",
            "moe_testing_set_layout_match",
            "moe_testing_set_dispatch_fused", "moe_testing_time_next_launch")
 
@@ -41,6 +45,10 @@ ABI_VERSION = 9
 # Quantised wire formats: name -> (code bits per value, values per scale byte).
 WIRE_FORMATS = {"mxfp8": (8, 32), "mxfp4": (4, 32), "nvfp4": (4, 16)}
 WIRE_CODES = {"mxfp8": 1, "mxfp4": 2, "nvfp4": 3}  # moe_dispatch_quantised's format
+
+LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+SCORINGS = {"softmax": 0, "sigmoid": 1}
+ACTS = {None: 0, "none": 0, "swiglu": 1}
 
 
 class MoeShape(ctypes.Structure):
@@ -114,6 +122,19 @@ def lib():
     L.moe_dispatch_quantised.argtypes = [shp, ctypes.c_int, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                          vp, vp, i64, vp, vp, vp, i64, vp, ctypes.c_size_t, vp,
                                          vp]
+    L.moe_route.restype = ctypes.c_int
+    L.moe_route.argtypes = [shp, vp, ctypes.c_int, vp, vp, vp, vp, vp, vp, vp]
+    L.moe_route_backward.restype = ctypes.c_int
+    L.moe_route_backward.argtypes = [shp, vp, ctypes.c_int, vp, vp, vp, vp, vp, vp, vp,
+                                     ctypes.c_int, vp, vp, vp]
+    L.moe_balance_loss.restype = ctypes.c_int
+    L.moe_balance_loss.argtypes = [shp, vp, ctypes.c_int, vp, vp, vp, ctypes.c_int, vp, vp, vp,
+                                   vp, vp, ctypes.c_size_t, vp, vp]
+    L.moe_balance_workspace_bytes.restype = ctypes.c_size_t
+    L.moe_balance_workspace_bytes.argtypes = [shp, ctypes.c_int]
+    L.moe_expert_product.restype = ctypes.c_int
+    L.moe_expert_product.argtypes = [shp, ctypes.c_int, ctypes.c_int, ctypes.c_int, vp, vp, vp,
+                                     i64, vp, vp, vp, vp, vp, vp]
     L.moe_testing_set_dispatch_fused.restype = ctypes.c_int
     L.moe_testing_set_dispatch_fused.argtypes = [ctypes.c_int]
     L.moe_testing_set_layout_form.restype = ctypes.c_int
@@ -561,6 +582,185 @@ def combine_ranks(partial, token_rank_slot, E: int, k: int, out, *, out_f32=None
         ctypes.byref(shape.c()), _ptr(_rows16(partial)), _ptr(_i32(token_rank_slot)),
         partial.shape[0], _ptr(_rows16(out)), _ptr(out_f32), _err(err), _stream(out.device))
     _check(st, "moe_combine_ranks")
+
+
+class Router(ctypes.Structure):
+    """moe_router_t: how the router scores, chooses and weighs. scoring
+    "softmax" or "sigmoid"; renorm: the weights are the chosen scores over
+    their sum; scale: a factor on them; groups / top_groups: the experts come
+    from the best top_groups of `groups` equal groups (sigmoid only)."""
+    _fields_ = [("scoring", ctypes.c_int32), ("renorm", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32)]
+
+    def __init__(self, scoring: str = "softmax", renorm: bool = True, scale: float = 1.0,
+                 groups: int = 1, top_groups: int = 1):
+        if scoring not in SCORINGS:
+            raise MoeError(f"unknown scoring {scoring!r}: one of {sorted(SCORINGS)}")
+        super().__init__(SCORINGS[scoring], 1 if renorm else 0, scale, groups, top_groups)
+
+
+def _dev(t: torch.Tensor | None, name: str, dtype, shape: tuple, device) -> int | None:
+    """The address of a tensor of exactly this type and shape, contiguous and
+    on `device`; None for None. Raises MoeError."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise MoeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise MoeError(f"{name} has shape {tuple(t.shape)}, the call needs {shape}")
+    if t.device != device:
+        raise MoeError(f"{name} is on {t.device}, the call needs {device}: all tensors must be "
+                       "on one GPU")
+    if not t.is_contiguous():
+        raise MoeError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _logits(logits: torch.Tensor, device) -> int:
+    """The type code of a [T, E] tensor of router logits on a GPU."""
+    if logits.dim() != 2 or logits.dtype not in LOGIT_TYPES:
+        raise MoeError("logits must be [T, E] of float32, bfloat16 or float16, got "
+                       f"{tuple(logits.shape)} of {logits.dtype}")
+    if device.type != "cuda":
+        raise MoeError("tensors must be on the GPU")
+    return LOGIT_TYPES[logits.dtype]
+
+
+def _call(fn, name: str, device, *args) -> None:
+    """One library call on the current stream of the tensors' device, which is
+    made current for it."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if st != MOE_OK:
+        _check(st, name)
+
+
+def route(logits: torch.Tensor, k: int, router: Router, topk_ids, topk_weights, *, bias=None,
+          token_mask=None, err=None) -> None:
+    """moe_route: the k experts of every token and their weights into
+    topk_ids [T, k] int32 and topk_weights [T, k] float32, from logits [T, E]
+    (float32, bfloat16 or float16); bias [E] float32 is added to the choice's
+    scores (sigmoid only); token_mask [T] bool or uint8: tokens with 0 get no
+    expert. The outputs are what layout() / dispatch_all() and combine() take."""
+    dev = logits.device
+    code = _logits(logits, dev)
+    T, E = logits.shape
+    if token_mask is not None and token_mask.dtype == torch.bool:
+        token_mask = token_mask.view(torch.uint8)
+    _check_err(err)
+    _call(lib().moe_route, "moe_route", dev, MoeShape(T, 8, E, 1, k), ctypes.byref(router), code,
+          _dev(logits, "logits", logits.dtype, (T, E), dev),
+          _dev(bias, "bias", torch.float32, (E,), dev),
+          _dev(token_mask, "token_mask", torch.uint8, (T,), dev),
+          _dev(topk_ids, "topk_ids", torch.int32, (T, k), dev),
+          _dev(topk_weights, "topk_weights", torch.float32, (T, k), dev), _err_ptr(err, dev))
+
+
+def _err_ptr(err: torch.Tensor | None, device) -> int | None:
+    return None if err is None else _dev(err, "err", torch.int32, err.shape, device)
+
+
+def route_backward(logits: torch.Tensor, topk_ids, router: Router, d_logits, *, d_weights=None,
+                   balance: tuple | None = None, err=None) -> None:
+    """moe_route_backward: the gradient of the logits into d_logits [T, E] (the
+    logits' type), from d_weights [T, k] float32 (the gradient of route()'s
+    weights), from the balance losses, or from both: `balance` is (d_loss [S]
+    float32, expert_counts [S, E], token_counts [S], seq_offsets [S + 1] or
+    None), with the counts balance_loss() gave."""
+    dev = logits.device
+    code = _logits(logits, dev)
+    T, E = logits.shape
+    if topk_ids.dim() != 2:
+        raise MoeError(f"topk_ids has shape {tuple(topk_ids.shape)}, the call needs [T, k]")
+    k = topk_ids.shape[1]
+    i32, f32 = torch.int32, torch.float32
+    S, d_loss, counts, tokens, offsets = 0, None, None, None, None
+    if d_weights is None and balance is None:
+        raise MoeError("give d_weights, balance or both")
+    if balance is not None:
+        d_loss, counts, tokens, offsets = balance
+        S = d_loss.numel()
+        d_loss = _dev(d_loss, "d_loss", f32, (S,), dev)
+        counts = _dev(counts, "expert_counts", i32, (S, E), dev)
+        tokens = _dev(tokens, "token_counts", i32, (S,), dev)
+        offsets = _dev(offsets, "seq_offsets", i32, (S + 1,), dev)
+    _check_err(err)
+    _call(lib().moe_route_backward, "moe_route_backward", dev, MoeShape(T, 8, E, 1, k),
+          ctypes.byref(router), code, _dev(logits, "logits", logits.dtype, (T, E), dev),
+          _dev(topk_ids, "topk_ids", i32, (T, k), dev),
+          _dev(d_weights, "d_weights", f32, (T, k), dev), d_loss, counts, tokens, offsets, S,
+          _dev(d_logits, "d_logits", logits.dtype, (T, E), dev), _err_ptr(err, dev))
+
+
+def balance_workspace_bytes(T: int, E: int, k: int, sequences: int = 1) -> int:
+    """moe_balance_workspace_bytes: scratch that balance_loss() needs."""
+    return int(lib().moe_balance_workspace_bytes(MoeShape(T, 8, E, 1, k), sequences))
+
+
+def balance_loss(logits: torch.Tensor, topk_ids, router: Router, loss, expert_counts,
+                 token_counts, score_mean, *, workspace, seq_offsets=None, err=None) -> None:
+    """moe_balance_loss: the balance loss of each of S sequences into loss [S]
+    float32, with expert_counts [S, E] int32 (pairs per expert), token_counts
+    [S] int32 and score_mean [S, E] float32. seq_offsets [S + 1] int32, or None
+    for one sequence of all tokens; workspace: a device tensor of at least
+    balance_workspace_bytes bytes."""
+    dev = logits.device
+    code = _logits(logits, dev)
+    T, E = logits.shape
+    if topk_ids.dim() != 2:
+        raise MoeError(f"topk_ids has shape {tuple(topk_ids.shape)}, the call needs [T, k]")
+    k, S = topk_ids.shape[1], loss.numel()
+    i32, f32 = torch.int32, torch.float32
+    _check_err(err)
+    _call(lib().moe_balance_loss, "moe_balance_loss", dev, MoeShape(T, 8, E, 1, k),
+          ctypes.byref(router), code, _dev(logits, "logits", logits.dtype, (T, E), dev),
+          _dev(topk_ids, "topk_ids", i32, (T, k), dev),
+          _dev(seq_offsets, "seq_offsets", i32, (S + 1,), dev), S,
+          _dev(loss, "loss", f32, (S,), dev),
+          _dev(expert_counts, "expert_counts", i32, (S, E), dev),
+          _dev(token_counts, "token_counts", i32, (S,), dev),
+          _dev(score_mean, "score_mean", f32, (S, E), dev),
+          _dev(workspace, "workspace", workspace.dtype, workspace.shape, dev),
+          workspace.numel() * workspace.element_size(), _err_ptr(err, dev))
+
+
+def expert_product(fmt: str, rows: torch.Tensor, expert_counts, expert_offsets, T: int, k: int,
+                   w_q, w_scale, out, *, act: str | None = None, factor=None, err=None) -> None:
+    """moe_expert_product: the rows [cap, H] (bf16) of the expert-grouped
+    buffer times their experts' 4-bit weights into out [cap, N] bf16, or
+    [cap, N / 2] with act "swiglu". fmt "mxfp4" or "nvfp4"; w_q [E, N, H / 2]
+    and w_scale [E, N, H / 32 or H / 16] uint8; factor [E] float32 multiplies
+    an expert's products; T * k bounds the rows in use. expert_counts [E] and
+    expert_offsets [E + 1] are the layout's, or those of the experts [a, b) of
+    it with their weights: counts[a:b], offsets[a:b + 1]."""
+    if fmt not in ("mxfp4", "nvfp4"):
+        raise MoeError(f"unknown weight format {fmt!r}: mxfp4 or nvfp4")
+    if act not in ACTS:
+        raise MoeError(f"unknown activation {act!r}: one of {sorted(a for a in ACTS if a)}")
+    dev = rows.device
+    if dev.type != "cuda":
+        raise MoeError("tensors must be on the GPU")
+    if rows.dim() != 2 or w_q.dim() != 3:
+        raise MoeError("rows must be [cap, H] and w_q [E, N, H / 2]")
+    cap, H = rows.shape
+    E, N, _ = w_q.shape
+    code = ACTS[act]
+    u8, i32 = torch.uint8, torch.int32
+    if rows.element_size() != 2 or out.element_size() != 2:
+        raise MoeError(f"expected 16-bit row tensors, got {rows.dtype} and {out.dtype}")
+    _check_err(err)
+    _call(lib().moe_expert_product, "moe_expert_product", dev, MoeShape(T, H, E, 1, k), N,
+          WIRE_CODES[fmt], code, _dev(rows, "rows", rows.dtype, (cap, H), dev),
+          _dev(expert_counts, "expert_counts", i32, (E,), dev),
+          _dev(expert_offsets, "expert_offsets", i32, (E + 1,), dev), cap,
+          _dev(w_q, "w_q", u8, (E, N, H // 2), dev),
+          _dev(w_scale, "w_scale", u8, (E, N, H // WIRE_FORMATS[fmt][1]), dev),
+          _dev(factor, "factor", torch.float32, (E,), dev),
+          _dev(out, "out", out.dtype, (cap, N // 2 if code else N), dev), _err_ptr(err, dev))
 
 
 def time_next_launch(start: "torch.cuda.Event | None", stop: "torch.cuda.Event | None") -> None:

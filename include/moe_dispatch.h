@@ -94,6 +94,8 @@ typedef enum moe_status {
 #define MOE_ERRBIT_BAD_ID 1         /* an id outside [-1, E) was skipped */
 #define MOE_ERRBIT_RANK_CAP 2       /* a copy at or past cap_rank was dropped */
 #define MOE_ERRBIT_EXPERT_CAP 4     /* a pair row at or past cap_expert was dropped or ignored */
+#define MOE_ERRBIT_BAD_LOGIT 8      /* a token with a NaN or +infinite logit was not routed */
+#define MOE_ERRBIT_BAD_SEQ 16       /* a sequence's offsets decrease or leave [0, T] */
 
 /* ABI version of the loaded library (MOE_DISPATCH_ABI_VERSION at build time). */
 int moe_abi_version(void);
@@ -441,6 +443,153 @@ int moe_combine_ranks(const moe_shape_t* shape, const uint16_t* partial,
                       float* out_f32, int32_t* err_word, void* stream);
 
 /*
+ * The router and the loss that balances it
+ *
+ * Logits are [T, E], row-major without padding, of one of three types; the
+ * arithmetic is in 32-bit floats or wider. -infinity masks an expert for a
+ * token: it is never chosen and its score is 0. Only T, E, R and k of the
+ * shape matter here.
+ */
+#define MOE_TYPE_F32 0
+#define MOE_TYPE_BF16 1
+#define MOE_TYPE_F16 2
+
+#define MOE_SCORE_SOFTMAX 0 /* s_e = exp(z_e) / sum over all E of exp(z) */
+#define MOE_SCORE_SIGMOID 1 /* s_e = 1 / (1 + exp(-z_e)) */
+
+typedef struct moe_router {
+  int32_t scoring;    /* MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID */
+  int32_t renorm;     /* 1: a token's weights are its scores over their sum; 0: the scores */
+  float scale;        /* factor on every weight, finite */
+  int32_t groups;     /* experts in this many equal consecutive groups (1..64, dividing E) */
+  int32_t top_groups; /* experts are chosen from the best top_groups groups (1..groups) */
+} moe_router_t;
+
+/*
+ * Router: the k experts of every token and their weights ([A2A] sec 1.1: the
+ * router scores all experts, picks the best k and gives each a weight).
+ *   The choice goes by a key per expert: with softmax scoring, and with sigmoid
+ *   scoring without bias and with one group, the logit itself; otherwise the
+ *   score 1 / (1 + exp(-z_e)) as the nearest float32, plus bias[e] (one float32
+ *   addition). The k largest keys are chosen, largest first, equal keys by the
+ *   lower id. With groups > 1 only the experts of the best top_groups groups
+ *   take part: a group's score is the sum of its two largest keys (its only
+ *   key where it has one), equal scores by the lower group. The weights are
+ *   made from the scores (the bias is not in them): scale * s_e, or scale *
+ *   s_e over the sum of the token's chosen scores (renorm).
+ *   An expert whose key is -infinity is never chosen; slots without an expert
+ *   get id -1 and weight 0. A token with a NaN or +infinite logit or key is
+ *   given no expert and flagged (MOE_ERRBIT_BAD_LOGIT).
+ *   logits_type      MOE_TYPE_F32, MOE_TYPE_BF16 or MOE_TYPE_F16
+ *   logits           [T*E] in
+ *   bias             [E] in:  float32 added to the keys, or NULL (sigmoid scoring only)
+ *   token_mask       [T] in:  bytes; a token with 0 is given no expert and its logits are
+ *                             not looked at (padding of a batch); or NULL
+ *   topk_ids [T*k], topk_weights [T*k]  out
+ * Bias and groups > 1 with softmax scoring are argument errors. One launch.
+ */
+int moe_route(const moe_shape_t* shape, const moe_router_t* router, int logits_type,
+              const void* logits, const float* bias, const uint8_t* token_mask,
+              int32_t* topk_ids, float* topk_weights, int32_t* err_word, void* stream);
+
+/*
+ * Gradient of the router's logits: from the gradient of the weights of
+ * moe_route (d_weights), from that of the losses of moe_balance_loss (d_loss),
+ * or the sum of both in one pass. The choice itself has no gradient.
+ *   logits, topk_ids  in: as moe_route read and wrote them (any ids in [-1, E) will
+ *                     do; several slots of one expert add up; ids outside are
+ *                     skipped and flagged, MOE_ERRBIT_BAD_ID)
+ *   d_weights         [T*k] in: or NULL; not read where the id is -1
+ *   d_loss            [sequences] in: or NULL; then the next four are not read
+ *   expert_counts [sequences*E], token_counts [sequences]   in: from moe_balance_loss
+ *   seq_offsets, sequences  as for moe_balance_loss
+ *   d_logits          [T*E] out: of the logits' type; every row is written (0 for a
+ *                     token with no expert). Must not overlap the logits.
+ * The counts are taken as constants, as the choice is. One launch.
+ */
+int moe_route_backward(const moe_shape_t* shape, const moe_router_t* router, int logits_type,
+                       const void* logits, const int32_t* topk_ids, const float* d_weights,
+                       const float* d_loss, const int32_t* expert_counts,
+                       const int32_t* token_counts, const int32_t* seq_offsets, int sequences,
+                       void* d_logits, int32_t* err_word, void* stream);
+
+/*
+ * Balance loss of every sequence, and what it is made of ([EP]: a layer is done
+ * when its busiest GPU is; a loss that grows with uneven expert loads trains the
+ * router to spread them). For sequence s, over its tokens with at least one
+ * expert (T' of them), with n_e the pairs of expert e and P_e the mean of the
+ * token's scores scaled to a sum of one (the softmax, or the sigmoids over
+ * their sum):
+ *   loss[s] = E / (k * T') * sum over e of n_e * P_e        (0 when T' = 0)
+ * which is 1 for even loads and scores. Sequence s is the tokens
+ * [seq_offsets[s], seq_offsets[s+1]); tokens outside all sequences, and tokens
+ * whose ids are all -1 (their logits are not looked at), count nowhere.
+ *   logits, topk_ids  in: as for moe_route_backward
+ *   seq_offsets       [sequences+1] in: non-decreasing, in [0, T]; or NULL with
+ *                     sequences = 1: all tokens. Offsets that are not are flagged
+ *                     (MOE_ERRBIT_BAD_SEQ) and the losses are then unspecified.
+ *   sequences         1..65,536
+ *   loss              [sequences] out
+ *   expert_counts     [sequences*E] out: n_e
+ *   token_counts      [sequences] out: T'
+ *   score_mean        [sequences*E] out: P_e
+ *   workspace         [workspace_bytes] scratch of moe_balance_workspace_bytes bytes or
+ *                     more, 16-byte aligned, as for moe_dispatch_layout (no clearing
+ *                     needed; not shared by calls that run at the same time)
+ * The sums do not depend on timing. Two launches.
+ */
+int moe_balance_loss(const moe_shape_t* shape, const moe_router_t* router, int logits_type,
+                     const void* logits, const int32_t* topk_ids, const int32_t* seq_offsets,
+                     int sequences, float* loss, int32_t* expert_counts, int32_t* token_counts,
+                     float* score_mean, void* workspace, size_t workspace_bytes,
+                     int32_t* err_word, void* stream);
+
+/* Bytes of workspace of moe_balance_loss; 0 for an invalid shape or count. */
+size_t moe_balance_workspace_bytes(const moe_shape_t* shape, int sequences);
+
+#define MOE_ACT_NONE 0   /* out = y */
+#define MOE_ACT_SWIGLU 1 /* out_i = y_i / (1 + exp(-y_i)) * y_(N/2 + i), N even */
+
+/*
+ * Expert products with 4-bit weights: every row x of the expert-grouped buffer
+ * times the weights of its expert, y = W_e x. It takes what moe_dispatch leaves
+ * (rows, counts, offsets) and writes the rows moe_combine reads, or, with an
+ * activation, the rows of the expert's next product. Made for decode-sized
+ * batches, where an expert has a few rows and the weights' bytes are the time;
+ * any number of rows is right.
+ *   Weights are in one of the two 4-bit wire formats of the quantised dispatch,
+ *   a row of W_e as a row of hidden states there: N rows of shape->H values,
+ *   H/2 bytes of e2m1 codes (the even value in the low nibble), and one scale
+ *   byte per 32 values (E8M0, MOE_WIRE_MXFP4) or per 16 (E4M3, MOE_WIRE_NVFP4).
+ *   The products are summed in 32-bit floats, the weights' values exact, and
+ *   rounded to bf16 once, after factor and activation.
+ *   shape          T*k bounds the number of rows in use, H is their width (a multiple
+ *                  of 32), E the experts whose weights are given; to use the experts
+ *                  [a, b) of a layout, pass E = b - a, expert_counts + a and
+ *                  expert_offsets + a. R, align and block are not looked at.
+ *   N              rows of one expert's weights (1 <= N; even with MOE_ACT_SWIGLU, whose
+ *                  gate is rows [0, N/2) and whose other factor rows [N/2, N))
+ *   format         MOE_WIRE_MXFP4 or MOE_WIRE_NVFP4;  act  MOE_ACT_NONE or MOE_ACT_SWIGLU
+ *   rows           [cap_expert*H] in: bf16, expert-grouped
+ *   expert_counts [E], expert_offsets [E+1]  in: from the layout (any of its three
+ *                  shapes); the rows of expert e are the first min(expert_counts[e],
+ *                  expert_offsets[e+1] - expert_offsets[e]) from expert_offsets[e];
+ *                  rows at or past cap_expert are skipped and flagged
+ *                  (MOE_ERRBIT_EXPERT_CAP)
+ *   w_q            [E*N*H/2] in: codes, 16-byte aligned
+ *   w_scale        [E*N*H/32] or [E*N*H/16] in: scale bytes, 16-byte aligned
+ *   factor         [E] in: float32 that multiplies y (a scale of the whole matrix), or NULL
+ *   out            [cap_expert*N], or [cap_expert*N/2] with MOE_ACT_SWIGLU, out: bf16,
+ *                  16-byte aligned; only the rows in use are written. Must not overlap rows.
+ * One launch.
+ */
+int moe_expert_product(const moe_shape_t* shape, int N, int format, int act,
+                       const uint16_t* rows, const int32_t* expert_counts,
+                       const int32_t* expert_offsets, int64_t cap_expert, const uint8_t* w_q,
+                       const uint8_t* w_scale, const float* factor, uint16_t* out,
+                       int32_t* err_word, void* stream);
+
+/*
  * Testing hook (not for production callers; it changes a process-wide setting
  * of this library and returns the previous value): which form of the layout
  * runs when a workspace is given: -1 (default) by size as described at
@@ -468,7 +617,8 @@ int moe_testing_set_dispatch_fused(int fused);
 
 /*
  * Measurement hook (not for production callers; process-wide, not
- * thread-safe): the next kernel this library launches, on any stream, has the
+ * thread-safe): the next kernel the dispatch and combine calls launch (the
+ * router, balance and expert calls leave it armed), on any stream, has the
  * runtime record start_event as it begins and stop_event as it ends, so that
  * hipEventElapsedTime(start_event, stop_event) is that kernel's own duration.
  * The events are the caller's (hipEvent_t as void*, created with timing
