@@ -1,10 +1,31 @@
 // Expert products with 4-bit weights: HIP kernels for CDNA4 (gfx950, wave64)
 // behind include/moe_dispatch.h.
 //
-// Kernel
-//  product_rows   one workgroup per (expert, column tile): reads the tile's
-//                 codes once for up to 32 rows of the buffer, expands them to
-//                 bf16 in registers and feeds them to MFMA
+// product_rows: out = W_e x for the rows x of the expert-grouped buffer. The
+// time of a decode batch is the weights' bytes, so everything goes by reading
+// each of them once, in whole cache lines, with the next ones on their way:
+//  - a workgroup takes a chunk of one expert's rows (4, 16, 32 or 64) and 32
+//    weight rows per wave; along H it goes in granules of 256 values, of which
+//    a wave has two on their way;
+//  - codes: a lane loads 16 bytes, 32 values of one weight row, so that a
+//    wave's two loads cover 128 bytes of each of 16 rows. Which values of H
+//    meet in one MFMA does not matter as long as both operands agree, so a
+//    lane's own 32 values are its part of four 16x16x32 MFMAs;
+//  - a word of 8 codes becomes 8 bf16 (exact: a code has 2 significant bits,
+//    an E4M3 scale 4) as MFMA's first operand: the weights are its rows, the
+//    buffer's rows its columns, of which a decode batch fills few;
+//  - scales come to LDS 128 bytes of a row at a time: read where they are
+//    used, a few bytes per row and granule, they cost 45 of 164 us at the
+//    decode size (their lines are gone from the cache before the next use);
+//  - the buffer's rows go through LDS, shared by the workgroup's waves. Read
+//    straight into registers they took 64 cache accesses an instruction (one
+//    per lane) and bounded the kernel: 190 us at that size.
+// Measured (kernel time; E = 48): one token's 6 experts, H = 5120, N = 4096,
+// SwiGLU, MXFP4 (67 MB) 16 us; 64 tokens in NVFP4 (566 MB) 128 us, 4.4 TB/s; H = 2048,
+// N = 5120 in MXFP4 (267 MB) 64 us, 4.2 TB/s; 256 tokens top-8 of E = 32, H =
+// 7168, N = 4096 in MXFP4 (499 MB, 64 rows an expert) 200 us. A kernel that only reads the codes
+// in this pattern takes 86 us and 47 us at the second and third size (5.9 and
+// 5.3 TB/s).
 
 #include "moe_common.h"
 
@@ -18,10 +39,8 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kBlock = 256;
-constexpr int kWaves = kBlock / kWave;
 constexpr int kTile = 16;    // an MFMA tile: 16 weight rows, 16 buffer rows
-constexpr int kNT = 2;       // tiles of weight rows per wave
+constexpr int NT = 2;        // tiles of weight rows per wave
 constexpr int kDepth = 2;    // granules of H that a wave has on their way
 constexpr int kChunk = 32;   // values of H in 16 bytes of codes
 
@@ -36,7 +55,8 @@ struct ProductArgs {
   int32_t* err;
   int64_t cap;
   int E, K, N, wide;  // wide: columns of out
-  int tiles, slots;   // column tiles, row chunks in the grid
+  int tiles;            // column tiles
+  int firsts, beyonds;  // slots of the grid for experts' first chunks, and for others
 };
 
 // Eight codes (a word) times a power of two, as bf16: exact, e2m1 has two
@@ -70,33 +90,52 @@ __device__ __forceinline__ bf16x8 expand_e4m3(uint32_t w, float scale) {
   return r;
 }
 
-// The first row of expert e in the buffer and how many are in use; rows the
-// buffer does not hold are left out.
-__device__ __forceinline__ int run_of(const ProductArgs& a, int e, int64_t* first) {
+// The first row of expert e in the buffer and how many are in use, without the
+// rows that the buffer does not hold (`over`: there are such).
+__device__ __forceinline__ int run_of(const ProductArgs& a, int e, int64_t* first, bool* over) {
   const int64_t begin = a.offsets[e], end = a.offsets[e + 1];
-  const int64_t n = min((int64_t)a.counts[e], end - begin);
+  const int64_t n = min((int64_t)a.counts[e], end - begin), held = min(n, a.cap - begin);
   *first = begin;
-  return ((begin < 0) | (n <= 0)) ? 0 : int(n);
+  *over = (begin >= 0) & (held < n) & (n > 0);
+  return ((begin < 0) | (held <= 0)) ? 0 : int(held);
 }
 
-// The expert of a slot: with as many slots as experts the slot itself, else
-// the slot-th expert that has rows (-1 when there are fewer); one wave looks
-// at 64 experts at a time.
-__device__ __forceinline__ int expert_of_slot(const ProductArgs& a, int slot) {
-  if (a.slots == a.E) return slot < a.E ? slot : -1;
+// The chunk of at most kRows rows that an index stands for, found by a wave
+// looking at 64 experts at a time: an expert's first chunk (`beyond` false), or
+// one of those it has beyond its first. False when there are no more.
+template <int kRows>
+__device__ __forceinline__ bool chunk_of(const ProductArgs& a, bool beyond, int at, int* expert,
+                                         int* chunk) {
   const int lane = lane_id();
-  for (int e0 = 0; e0 < a.E; e0 += kWave) {
-    const int e = min(e0 + lane, a.E - 1);
-    int64_t first;
-    const uint64_t live = __ballot(run_of(a, e, &first) > 0 && e0 + lane < a.E);
-    const int n = __popcll(live);
-    if (slot < n) {
-      const bool at = ((live >> lane) & 1) && __popcll(live & ((uint64_t(1) << lane) - 1)) == slot;
-      return e0 + __ffsll((unsigned long long)__ballot(at)) - 1;
-    }
-    slot -= n;
+  *chunk = 0;
+  if (!beyond && a.firsts == a.E) {  // a slot for each expert: no need to look
+    *expert = at;
+    return at < a.E;
   }
-  return -1;
+  for (int e0 = 0; e0 < a.E; e0 += kWave) {
+    int64_t first;
+    bool over;
+    const int run = run_of(a, min(e0 + lane, a.E - 1), &first, &over);
+    int n = run / kRows + (run % kRows > 0 ? 1 : 0);
+    n = e0 + lane >= a.E ? 0 : beyond ? max(0, n - 1) : min(1, n);
+    int before = n;  // becomes the sum over the lanes up to this one
+    for (int s = 1; s < kWave; s <<= 1) {
+      const int up = __shfl_up(before, s);
+      if (lane >= s) before += up;
+    }
+    const int total = read_lane(before, kWave - 1);
+    before -= n;
+    if (at < total) {
+      const uint64_t hit = __ballot(at >= before && at < before + n);
+      if (!hit) return false;  // counts of no layout, whose sum has overflowed
+      const int l = __ffsll((unsigned long long)hit) - 1;
+      *expert = e0 + l;
+      if (beyond) *chunk = 1 + at - read_lane(before, l);
+      return true;
+    }
+    at -= total;
+  }
+  return false;
 }
 
 typedef __amdgpu_buffer_rsrc_t buffer;
@@ -124,75 +163,93 @@ __device__ __forceinline__ int offset_if(bool in, int off) {
 // part of the granule of the buffer's rows.
 template <int NX>
 struct Stage {
-  vec4 code[2][kNT];
+  vec4 code[2][NT];
   vec4 x[NX];
 };
 
-// Scales: 128 bytes of each of the wave's 32 weight rows at a time, a cache
+// Scales: 128 bytes of each of the wave's weight rows at a time, a cache
 // line's worth, into the wave's LDS (rows 144 bytes apart: 16 rows' same bytes
 // in different banks).
 constexpr int kScaleRow = 144;
-constexpr int kScaleBytes = kNT * kTile * kScaleRow;
 
-// The rows of the weights, of a granule of the buffer rows in LDS, and their
-// products.
-template <bool kE4M3, bool kSwiglu, int WK, int MT>
-__global__ __launch_bounds__(kBlock, MT == 1 ? 3 : 2) void product_rows(ProductArgs a) {
+// Where 16-byte piece p (0..31) of row r of a granule lies in LDS. A 16-byte
+// read is served for 16 lanes at a time, taken from two neighbouring groups of
+// 16: (m, kq) with kq = 0 for half of the m and kq = 1 for the other half. With
+// kq in the low bits of the place and the row folded in, these 16 lie in
+// different banks.
+__device__ __forceinline__ int piece_at(int r, int p) {
+  const int place = (p & 16) | (p & 3) << 2 | (p >> 2 & 3);
+  return r * 512 + (place ^ (r & 15)) * 16;
+}
+
+// W waves per workgroup. WK = 1: they share kRows rows of the buffer and take
+// NT tiles of weight rows each. WK = W: they take a part of H each, of the same
+// NT tiles.
+template <bool kE4M3, bool kSwiglu, int W, int WK, int MT>
+__global__ __launch_bounds__(W * kWave, MT == 1 ? 3 : 2) void product_rows(ProductArgs a) {
+  static_assert(WK == 1 || (WK == W && MT == 1 && W == 4), "waves split N, or all of them H");
+  constexpr int kThreads = W * kWave;
   constexpr int kRows = WK == 1 ? kTile * MT : 4;        // buffer rows at a time
-  constexpr int kSharers = WK == 1 ? kBlock : kWave;     // threads that stage them
+  constexpr int kSharers = WK == 1 ? kThreads : kWave;   // threads that stage them
   constexpr int NX = kRows * 32 / kSharers;              // 16-byte pieces per thread
   constexpr int kSlot = kRows * 512;                     // bytes of a granule of them
-  constexpr int kSlots = 2 * (WK == 1 ? 1 : kWaves);
-  static_assert(WK == 1 || (WK == kWaves && MT == 1), "waves split N, or all of them H");
-  __shared__ __align__(16) char staged[kSlots * kSlot];
-  __shared__ __align__(16) uint8_t scales[kWaves][kScaleBytes];
-  __shared__ float part[WK == 1 ? 1 : kWaves][kNT * 4][kWave];
+  constexpr int kCols = kTile * (kSwiglu ? NT / 2 : NT); // columns of out per wave
+  constexpr int kPerGranule = kE4M3 ? 16 : 8;            // scale bytes of a weight row
+  constexpr int kSuper = 128 / kPerGranule;              // granules whose scales are in LDS
+  constexpr int NS = NT * kTile / 8;                     // 16-byte loads of them per lane
+  static_assert(kSuper % kDepth == 0, "scales are renewed between rounds of the ring");
+  static_assert(kDepth % 2 == 0, "a granule of the ring has a slot of the two");
+  __shared__ __align__(16) char staged[2 * (WK == 1 ? 1 : W) * kSlot];
+  __shared__ __align__(16) uint8_t scales[W][NT * kTile * kScaleRow];
+  __shared__ float part[WK == 1 ? 1 : W][NT * 4][WK == 1 ? 1 : kWave];
   const int lane = lane_id(), wave = wave_in_block();
   const int m = lane & 15, kq = lane >> 4;
-  const int tile = blockIdx.x % a.tiles;
   const int nchunks = a.K / kChunk;
-  const int stages = ((nchunks + 7) / 8 + WK - 1) / WK;  // granules per wave
+  const int stages = ((nchunks + 7) / 8 + WK - 1) / WK;  // granules of a wave
   const int half = a.N / 2;
   const int limit = kSwiglu ? half : a.N;                // columns of y (of each factor)
   const int srow = kE4M3 ? a.K / 16 : a.K / 32;          // scale bytes per weight row
-  const int wn = WK == 1 ? wave : 0, wk = WK == 1 ? 0 : wave;
-  constexpr int kPerGranule = kE4M3 ? 16 : 8;  // scale bytes of a row
-  constexpr int kSuper = 128 / kPerGranule;    // granules whose scales are in LDS
-  static_assert(kSuper % kDepth == 0, "scales are renewed between rounds of the ring");
-  const int g0 = wk * stages;                  // the wave's first granule,
-  const int end = min(nchunks, 8 * (g0 + stages));  // and the end of its chunks
+  const int g0 = WK == 1 ? 0 : wave * stages;            // the wave's first granule,
+  const int end = min(nchunks, 8 * (g0 + stages));       // and the end of its chunks
   uint8_t* sc = scales[wave];
   const int64_t scale_bytes = (int64_t)a.E * a.N * srow;
   char* lds = staged + (WK == 1 ? 0 : wave * 2 * kSlot);
-  const int n0 = (tile * (kWaves / WK) + wn) * kTile * (kSwiglu ? 1 : kNT);
+  const int sharer = WK == 1 ? threadIdx.x : lane;
 
-  for (int slot = blockIdx.x / a.tiles;; slot += a.slots) {
-    const int e = __builtin_amdgcn_readfirstlane(expert_of_slot(a, slot));
-    if (e < 0) return;
+  // The first weight row of tile h of this wave, and how many rows it has
+  // (none past the last column).
+  const int n0 = (blockIdx.x % a.tiles * (W / WK) + (WK == 1 ? wave : 0)) * kCols;
+  auto row_of = [&](int h) {
+    return kSwiglu ? n0 + h / 2 * kTile + h % 2 * half : n0 + h * kTile;
+  };
+
+  // The last `beyonds` slots take what experts have beyond a first chunk.
+  const int slot = blockIdx.x / a.tiles;
+  const bool beyond = slot >= a.firsts;
+  for (int index = beyond ? slot - a.firsts : slot;; index += beyond ? a.beyonds : a.firsts) {
+    int e, chunk;
+    if (!chunk_of<kRows>(a, beyond, index, &e, &chunk)) return;
+    e = __builtin_amdgcn_readfirstlane(e);
+    chunk = __builtin_amdgcn_readfirstlane(chunk);
     int64_t first;
-    int run = run_of(a, e, &first);
-    if (run > 0 && first + run > a.cap) {
-      if (threadIdx.x == 0) flag_error(a.err, MOE_ERRBIT_EXPERT_CAP);
-      run = first < a.cap ? int(a.cap - first) : 0;
-    }
-    run = __builtin_amdgcn_readfirstlane(run);
+    bool over;
+    const int run = __builtin_amdgcn_readfirstlane(run_of(a, e, &first, &over));
+    if (over && threadIdx.x == 0) flag_error(a.err, MOE_ERRBIT_EXPERT_CAP);
+    first = (int64_t)__builtin_amdgcn_readfirstlane((int)first);  // offsets are int32
 
-    buffer wq[kNT];  // this wave's tiles of the weights, and their scales
-    int64_t ws[kNT];
+    buffer wq[NT];  // this wave's weight rows
 #pragma unroll
-    for (int h = 0; h < kNT; ++h) {
-      const int n = n0 + (kSwiglu ? 0 : h * kTile);
-      const int64_t r = (int64_t)e * a.N + n + (kSwiglu ? h * half : 0);
-      const int rows = max(0, min(kTile, limit - n));
-      wq[h] = make_buffer(a.w_q + r * (a.K / 2), rows * (a.K / 2));
-      ws[h] = r * srow;
+    for (int h = 0; h < NT; ++h) {
+      const int n = n0 + (kSwiglu ? h / 2 : h) * kTile;
+      wq[h] = make_buffer(a.w_q + ((int64_t)e * a.N + row_of(h)) * (a.K / 2),
+                          max(0, min(kTile, limit - n)) * (a.K / 2));
     }
 
-    for (int r0 = 0; r0 < run; r0 += kRows) {
+    // one chunk; all of them where the grid has no slots for the others
+    for (int r0 = chunk * kRows; r0 < run; r0 += a.beyonds > 0 ? run : kRows) {
       const int nr = min(kRows, run - r0);
-      const int64_t row0 = __builtin_amdgcn_readfirstlane((int)first) + (int64_t)r0;
+      const int64_t row0 = first + r0;
       const buffer xb = make_buffer(a.rows + row0 * a.K, nr * a.K * 2);
-      const int sharer = WK == 1 ? threadIdx.x : lane;
 
       // The loads of a stage stay together and in the order of the stages: a
       // wait for one stage then leaves the later ones on their way.
@@ -210,73 +267,75 @@ __global__ __launch_bounds__(kBlock, MT == 1 ? 3 : 2) void product_rows(ProductA
           const int c = 8 * g + 4 * u + kq;
           const int off = offset_if(c < end, m * (a.K / 2) + c * 16);
 #pragma unroll
-          for (int h = 0; h < kNT; ++h)
+          for (int h = 0; h < NT; ++h)
             f.code[u][h] =
                 __builtin_bit_cast(vec4, __builtin_amdgcn_raw_buffer_load_b128(wq[h], off, 0, 0));
         }
         __builtin_amdgcn_sched_barrier(0);
       };
-
-      // The scales of granules [g0 + s, g0 + s + kSuper) to LDS: 8 lanes a row,
-      // 16 bytes from any address each, held within the scales of all experts
-      // (what a row's end or a row past N leaves there is not used). A piece
-      // that the end of the scales cuts off is read again byte by byte.
+      // The scales of granules [g0 + s, g0 + s + kSuper): 8 lanes a row, 16
+      // bytes from any address each, held within the scales of all experts
+      // (what a row's end or a row past N leaves there is not used).
+      vec4 sv[NS];
+      auto scale_place = [&](int s, int i) {
+        return ((int64_t)e * a.N + row_of(i / 2) + 8 * (i % 2) + (lane >> 3)) * srow +
+               (g0 + s) * kPerGranule + 16 * (lane & 7);
+      };
       auto load_scales = [&](int s) {
-        vec4 v[kNT * kTile / 8];
-        bool cut = false;
-        auto place = [&](int i) {
-          const int h = i / 2, r = 8 * (i % 2) + (lane >> 3);
-          return (h ? ws[1] : ws[0]) + r * srow + (g0 + s) * kPerGranule + 16 * (lane & 7);
-        };
 #pragma unroll
-        for (int i = 0; i < kNT * kTile / 8; ++i) {
-          const int64_t at = place(i);
-          cut |= at < scale_bytes && at > scale_bytes - 16;
-          v[i] = vec4{0, 0, 0, 0};
+        for (int i = 0; i < NS; ++i) {
+          sv[i] = vec4{0, 0, 0, 0};
           if (scale_bytes >= 16)  // uniform
-            __builtin_memcpy(&v[i], a.w_scale + min(at, scale_bytes - 16), 16);
+            __builtin_memcpy(&sv[i], a.w_scale + min(scale_place(s, i), scale_bytes - 16), 16);
         }
+      };
+      // Into LDS; a piece that the end of the scales cuts off is read again
+      // byte by byte.
+      auto store_scales = [&](int s) {
         uint8_t* to = sc + (lane >> 3) * kScaleRow + 16 * (lane & 7);
+        bool cut = false;
 #pragma unroll
-        for (int i = 0; i < kNT * kTile / 8; ++i)
-          *reinterpret_cast<vec4*>(to + i * 8 * kScaleRow) = v[i];
+        for (int i = 0; i < NS; ++i) {
+          *reinterpret_cast<vec4*>(to + i * 8 * kScaleRow) = sv[i];
+          const int64_t at = scale_place(s, i);
+          cut |= at < scale_bytes && at > scale_bytes - 16;
+        }
         if (__ballot(cut)) {
 #pragma unroll 1
-          for (int i = 0; i < kNT * kTile / 8; ++i)
+          for (int i = 0; i < NS; ++i)
 #pragma unroll 1
             for (int q = 0; q < 16; ++q) {
-              const int64_t at = place(i) + q;
+              const int64_t at = scale_place(s, i) + q;
               if (at < scale_bytes) to[i * 8 * kScaleRow + q] = a.w_scale[at];
             }
         }
         __builtin_amdgcn_wave_barrier();
       };
 
-      f32x4 acc[kNT][MT];
-#pragma unroll
-      for (int h = 0; h < kNT; ++h)
-#pragma unroll
-        for (int q = 0; q < MT; ++q) acc[h][q] = f32x4{0, 0, 0, 0};
-
       // kDepth granules are on their way at any time. One past the last reads
       // nothing and adds 0.
       Stage<NX> f[kDepth];
+      load_scales(0);
 #pragma unroll
       for (int d = 0; d < kDepth; ++d) load(f[d], d);
+      f32x4 acc[NT][MT];
+#pragma unroll
+      for (int h = 0; h < NT; ++h)
+#pragma unroll
+        for (int q = 0; q < MT; ++q) acc[h][q] = f32x4{0, 0, 0, 0};
       for (int s0 = 0; s0 < stages; s0 += kDepth) {
-        if (s0 % kSuper == 0) load_scales(s0);
+        if (s0 % kSuper == 0) store_scales(s0);
+        if ((s0 + kDepth) % kSuper == 0) load_scales(s0 + kDepth);
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) {
           const int s = s0 + d;
           // The granule's rows to LDS, two slots in turn: the one written here
-          // was last read before the barrier of the granule before. Piece p of
-          // row r lies at place p ^ r, so that the rows' same pieces are in
-          // different banks.
-          char* at = lds + (s & 1) * kSlot;
+          // was last read before the barrier of the granule before.
+          char* at = lds + d % 2 * kSlot;
 #pragma unroll
           for (int i = 0; i < NX; ++i) {
             const int r = (sharer + i * kSharers) >> 5, p = sharer & 31;
-            *reinterpret_cast<vec4*>(at + r * 512 + ((p ^ (r & 15)) * 16)) = f[d].x[i];
+            *reinterpret_cast<vec4*>(at + piece_at(r, p)) = f[d].x[i];
           }
           if (WK == 1)
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -287,28 +346,24 @@ __global__ __launch_bounds__(kBlock, MT == 1 ? 3 : 2) void product_rows(ProductA
             // this lane's chunk: its scale, 0 past H (a code there is 0, but
             // 0 times a NaN scale would not be)
             const bool in = 8 * (g0 + s) + 4 * u + kq < end;
-            uint32_t b[kNT];
+            uint32_t b[NT];
 #pragma unroll
-            for (int h = 0; h < kNT; ++h) {
+            for (int h = 0; h < NT; ++h) {
               const uint8_t* p = sc + (h * kTile + m) * kScaleRow + (s % kSuper) * kPerGranule;
               const uint32_t v = kE4M3 ? *reinterpret_cast<const uint16_t*>(p + 8 * u + 2 * kq)
                                        : p[4 * u + kq];
               b[h] = in ? v : 0;
             }
-            bf16x8 x[MT][4];
 #pragma unroll
-            for (int q = 0; q < MT; ++q) {
-              if (q > 0 && nr <= q * kTile) break;  // uniform: no rows there
+            for (int j = 0; j < 4; ++j) {
+              bf16x8 x[MT];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
+              for (int q = 0; q < MT; ++q) {
                 const int r = WK == 1 ? q * kTile + m : m & 3, p = 16 * u + 4 * kq + j;
-                x[q][j] = *reinterpret_cast<const bf16x8*>(at + r * 512 + (p ^ (r & 15)) * 16);
+                x[q] = *reinterpret_cast<const bf16x8*>(at + piece_at(r, p));
               }
-            }
 #pragma unroll
-            for (int h = 0; h < kNT; ++h)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
+              for (int h = 0; h < NT; ++h) {
                 const uint32_t code = f[d].code[u][h][j];
                 bf16x8 w;
                 if (kE4M3)
@@ -318,75 +373,98 @@ __global__ __launch_bounds__(kBlock, MT == 1 ? 3 : 2) void product_rows(ProductA
                   w = expand_e8m0(code, __uint_as_float(b[h] << 23));
 #pragma unroll
                 for (int q = 0; q < MT; ++q) {
-                  if (q > 0 && nr <= q * kTile) break;
-                  acc[h][q] =
-                      __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x[q][j], acc[h][q], 0, 0, 0);
+                  acc[h][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x[q], acc[h][q], 0, 0, 0);
                 }
               }
+            }
           }
           load(f[d], s + kDepth);
         }
       }
 
+      // y to out: lane (m, kq) holds rows 16 q + m, columns 4 kq .. 4 kq + 3 of
+      // each tile
       const float factor = a.factor ? a.factor[e] : 1.0f;
-      __bf16* out = reinterpret_cast<__bf16*>(a.out) + row0 * a.wide;
+      auto put = [&](int r, int h, int i, float y, float up) {
+        const int n = n0 + (kSwiglu ? h / 2 : h) * kTile + 4 * kq + i;
+        if (r >= nr || n >= limit) return;
+        if (kSwiglu) y = y / (1.0f + expf(-y)) * up;
+        reinterpret_cast<__bf16*>(a.out)[(row0 + r) * a.wide + n] = __bf16(y);
+      };
       if (WK == 1) {
 #pragma unroll
-        for (int q = 0; q < MT; ++q) {
-          const int r = q * kTile + m;
-          if (r >= nr) continue;
+        for (int q = 0; q < MT; ++q)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int n = n0 + 4 * kq + i;
-            const float y0 = acc[0][q][i] * factor, y1 = acc[1][q][i] * factor;
-            if (kSwiglu) {
-              if (n < half) out[(int64_t)r * a.wide + n] = __bf16(y0 / (1.0f + expf(-y0)) * y1);
-            } else {
-              if (n < a.N) out[(int64_t)r * a.wide + n] = __bf16(y0);
-              if (n + kTile < a.N) out[(int64_t)r * a.wide + n + kTile] = __bf16(y1);
-            }
-          }
-        }
+          for (int h = 0; h < NT; h += kSwiglu ? 2 : 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              put(q * kTile + m, h, i, acc[h][q][i] * factor, acc[(h + 1) % NT][q][i] * factor);
+        // LDS is written anew when every wave is done with it
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       } else {
         // join the waves' parts: thread (wave i, lane) adds up element i of
         // every fragment of that lane, in wave order
 #pragma unroll
-        for (int h = 0; h < kNT; ++h)
+        for (int h = 0; h < NT; ++h)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) part[wave][h * 4 + i][lane] = acc[h][0][i];
+          for (int i = 0; i < 4; ++i)
+            part[WK == 1 ? 0 : wave][h * 4 + i][WK == 1 ? 0 : lane] = acc[h][0][i];
         __syncthreads();
-        float y[kNT];
+        float y[NT];
 #pragma unroll
-        for (int h = 0; h < kNT; ++h) {
+        for (int h = 0; h < NT; ++h) {
           y[h] = 0.0f;
 #pragma unroll
-          for (int w = 0; w < (WK == 1 ? 1 : kWaves); ++w) y[h] += part[w][h * 4 + wave][lane];
+          for (int w = 0; w < (WK == 1 ? 1 : W); ++w)
+            y[h] += part[w][h * 4 + (wave & 3)][WK == 1 ? 0 : lane];
           y[h] *= factor;
         }
-        const int n = n0 + 4 * kq + wave;
-        if (m < nr) {
-          if (kSwiglu) {
-            if (n < half) out[(int64_t)m * a.wide + n] = __bf16(y[0] / (1.0f + expf(-y[0])) * y[1]);
-          } else {
-            if (n < a.N) out[(int64_t)m * a.wide + n] = __bf16(y[0]);
-            if (n + kTile < a.N) out[(int64_t)m * a.wide + n + kTile] = __bf16(y[1]);
-          }
-        }
+#pragma unroll
+        for (int h = 0; h < NT; h += kSwiglu ? 2 : 1) put(m, h, wave, y[h], y[(h + 1) % NT]);
         __syncthreads();
       }
     }
   }
 }
 
+// Forms of the kernel: waves, waves over H, tiles of buffer rows.
+struct Form {
+  int waves, over_h, rows;  // rows: of the buffer at a time
+};
+constexpr Form kForms[] = {{4, 4, 4}, {4, 1, 16}, {8, 1, 32}, {8, 1, 64}};
+
 template <bool kE4M3, bool kSwiglu>
-void launch_product(int wk, int mt, dim3 grid, hipStream_t st, const ProductArgs& a) {
-  if (wk == kWaves)
-    product_rows<kE4M3, kSwiglu, kWaves, 1><<<grid, kBlock, 0, st>>>(a);
-  else if (mt == 1)
-    product_rows<kE4M3, kSwiglu, 1, 1><<<grid, kBlock, 0, st>>>(a);
-  else
-    product_rows<kE4M3, kSwiglu, 1, 2><<<grid, kBlock, 0, st>>>(a);
+void launch_product(int form, dim3 grid, hipStream_t st, const ProductArgs& a) {
+  const int threads = kForms[form].waves * kWave;
+  switch (form) {
+    case 0: product_rows<kE4M3, kSwiglu, 4, 4, 1><<<grid, threads, 0, st>>>(a); break;
+    case 1: product_rows<kE4M3, kSwiglu, 4, 1, 1><<<grid, threads, 0, st>>>(a); break;
+    case 2: product_rows<kE4M3, kSwiglu, 8, 1, 2><<<grid, threads, 0, st>>>(a); break;
+    default: product_rows<kE4M3, kSwiglu, 8, 1, 4><<<grid, threads, 0, st>>>(a);
+  }
+}
+
+int column_tiles(int form, bool swiglu, int wide) {
+  const int cols = kTile * (swiglu ? NT / 2 : NT) * kForms[form].waves / kForms[form].over_h;
+  return (wide + cols - 1) / cols;
+}
+
+// By the mean number of rows of an expert that has any (uniform routing at
+// worst): as many rows at a time as that takes, since every chunk of rows
+// reads the codes again. Measured at E = 48, H = 5120, N = 4096 with SwiGLU in
+// MXFP4, mean rows 2 / 6 / 8 / 12 / 24 / 32: 16 rows 80 / 101 / 113 / 130 /
+// 195 / 236 us, 32 rows 102 / 109 / 110 / 123 / 152 / 183 us, 64 rows 122 /
+// 126 / 130 / 133 / 152 / 171 us (H = 2048, N = 5120 in NVFP4 alike).
+// Few workgroups with long rows split H over the waves instead of columns:
+// 16.3 against 18.6 us for one token's 6 experts there (192 workgroups), 27
+// against 30 us for two tokens', but 49.1 against 49.2 us for four (768), and
+// at H = 2048 14.8 against 14.3 us for one.
+int form_of(const moe_shape_t& sh, bool swiglu, int wide, int64_t pairs, int64_t active) {
+  const int64_t mean = (pairs + active - 1) / active;
+  if (mean > 24) return 3;
+  if (mean > 10) return 2;
+  const bool few = active * column_tiles(1, swiglu, wide) < 512;
+  return mean <= 2 && few && sh.H >= 4096 ? 0 : 1;
 }
 
 }  // namespace
@@ -401,7 +479,7 @@ int moe_expert_product(const moe_shape_t* shape, int N, int format, int act,
   if (!shape_ok(shape) || shape->H % kChunk != 0) return MOE_ERR_ARG;
   if (format != MOE_WIRE_MXFP4 && format != MOE_WIRE_NVFP4) return MOE_ERR_ARG;
   if (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU) return MOE_ERR_ARG;
-  if (N < 1 || N > (1 << 24) || (act == MOE_ACT_SWIGLU && N % 2 != 0)) return MOE_ERR_ARG;
+  if (shape->H > (1 << 20) || N < 1 || N > (1 << 24) || (act == MOE_ACT_SWIGLU && N % 2 != 0)) return MOE_ERR_ARG;
   if (cap_expert < 0) return MOE_ERR_ARG;
   const int64_t pairs = int64_t(shape->T) * shape->k;
   if (pairs == 0) return MOE_OK;
@@ -413,26 +491,25 @@ int moe_expert_product(const moe_shape_t* shape, int N, int format, int act,
   const bool swiglu = act == MOE_ACT_SWIGLU;
   const int wide = swiglu ? N / 2 : N;
   const int64_t active = std::min<int64_t>(shape->E, pairs);
-  const int64_t per = (pairs + active - 1) / active;
-  const int wk = per <= 2 ? kWaves : 1;
-  const int mt = per <= 6 ? 1 : 2;
-  const int cols = kTile * (swiglu ? 1 : kNT) * (kWaves / wk);
-  const int tiles = (wide + cols - 1) / cols;
-  const int64_t slots = std::min<int64_t>(active, int64_t(INT32_MAX) / tiles);
+  const int form = form_of(*shape, swiglu, wide, pairs, active);
+  const int tiles = column_tiles(form, swiglu, wide);
+  const int64_t most = INT32_MAX / tiles / 2;
+  const int firsts = int(std::min(active, most));
+  const int beyonds = int(std::min((pairs - 1) / kForms[form].rows, most));
   const ProductArgs a{rows, expert_counts, expert_offsets, w_q, w_scale, factor, out, err_word,
-                      cap_expert, shape->E, shape->H, N, wide, tiles, int(slots)};
-  const dim3 grid(uint32_t(slots * tiles));
+                      cap_expert, shape->E, shape->H, N, wide, tiles, firsts, beyonds};
+  const dim3 grid(uint32_t(firsts + beyonds) * tiles);
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (format == MOE_WIRE_NVFP4) {
     if (swiglu)
-      launch_product<true, true>(wk, mt, grid, st, a);
+      launch_product<true, true>(form, grid, st, a);
     else
-      launch_product<true, false>(wk, mt, grid, st, a);
+      launch_product<true, false>(form, grid, st, a);
   } else {
     if (swiglu)
-      launch_product<false, true>(wk, mt, grid, st, a);
+      launch_product<false, true>(form, grid, st, a);
     else
-      launch_product<false, false>(wk, mt, grid, st, a);
+      launch_product<false, false>(form, grid, st, a);
   }
   return launch_status();
 }

@@ -564,10 +564,10 @@ size_t moe_balance_workspace_bytes(const moe_shape_t* shape, int sequences);
  *   The products are summed in 32-bit floats, the weights' values exact, and
  *   rounded to bf16 once, after factor and activation.
  *   shape          T*k bounds the number of rows in use, H is their width (a multiple
- *                  of 32), E the experts whose weights are given; to use the experts
+ *                  of 32, at most 2^20), E the experts whose weights are given; to use the experts
  *                  [a, b) of a layout, pass E = b - a, expert_counts + a and
  *                  expert_offsets + a. R, align and block are not looked at.
- *   N              rows of one expert's weights (1 <= N; even with MOE_ACT_SWIGLU, whose
+ *   N              rows of one expert's weights (1 <= N <= 2^24; even with MOE_ACT_SWIGLU, whose
  *                  gate is rows [0, N/2) and whose other factor rows [N/2, N))
  *   format         MOE_WIRE_MXFP4 or MOE_WIRE_NVFP4;  act  MOE_ACT_NONE or MOE_ACT_SWIGLU
  *   rows           [cap_expert*H] in: bf16, expert-grouped
