@@ -10,6 +10,7 @@ tensors are not on a GPU, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -47,6 +48,7 @@ WIRE_FORMATS = {"mxfp8": (8, 32), "mxfp4": (4, 32), "nvfp4": (4, 16)}
 WIRE_CODES = {"mxfp8": 1, "mxfp4": 2, "nvfp4": 3}  # moe_dispatch_quantised's format
 
 LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+ROW_TYPES = (torch.bfloat16, torch.int16, torch.uint16)  # of the expert products' rows
 SCORINGS = {"softmax": 0, "sigmoid": 1}
 ACTS = {None: 0, "none": 0, "swiglu": 1}
 
@@ -600,11 +602,35 @@ class Router(ctypes.Structure):
         super().__init__(SCORINGS[scoring], 1 if renorm else 0, scale, groups, top_groups)
 
 
+# The raw stream and device of the caller's context, without the objects that
+# torch.cuda.current_stream() makes at every call (2 us of a 9 us call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _current_stream(device: torch.device) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _current_device() -> int:
+    return _raw_device() if _raw_device is not None else torch.cuda.current_device()
+
+
+@functools.lru_cache(maxsize=1024)
+def _sizes(T: int, H: int, E: int, k: int) -> MoeShape:
+    """The shape structure of a call (only ever read by the library)."""
+    return MoeShape(T, H, E, 1, k)
+
+
 def _dev(t: torch.Tensor | None, name: str, dtype, shape: tuple, device) -> int | None:
     """The address of a tensor of exactly this type and shape, contiguous and
     on `device`; None for None. Raises MoeError."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise MoeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -612,29 +638,36 @@ def _dev(t: torch.Tensor | None, name: str, dtype, shape: tuple, device) -> int 
     if t.device != device:
         raise MoeError(f"{name} is on {t.device}, the call needs {device}: all tensors must be "
                        "on one GPU")
-    if not t.is_contiguous():
-        raise MoeError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise MoeError(f"{name} must be contiguous")
+
+
+def _dev_err(t: torch.Tensor | None, device) -> int | None:
+    """The address of the device error word (see _check_err)."""
+    if t is None:
+        return None
+    _check_err(t)
+    return _dev(t, "err", torch.int32, t.shape, device)
 
 
 def _logits(logits: torch.Tensor, device) -> int:
     """The type code of a [T, E] tensor of router logits on a GPU."""
-    if logits.dim() != 2 or logits.dtype not in LOGIT_TYPES:
+    code = LOGIT_TYPES.get(logits.dtype)
+    if code is None or logits.dim() != 2:
         raise MoeError("logits must be [T, E] of float32, bfloat16 or float16, got "
                        f"{tuple(logits.shape)} of {logits.dtype}")
     if device.type != "cuda":
         raise MoeError("tensors must be on the GPU")
-    return LOGIT_TYPES[logits.dtype]
+    return code
 
 
 def _call(fn, name: str, device, *args) -> None:
     """One library call on the current stream of the tensors' device, which is
     made current for it."""
-    if device.index != torch.cuda.current_device():
+    if device.index != _current_device():
         with torch.cuda.device(device):
-            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            st = fn(*args, _current_stream(device))
     else:
-        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        st = fn(*args, _current_stream(device))
     if st != MOE_OK:
         _check(st, name)
 
@@ -651,17 +684,12 @@ def route(logits: torch.Tensor, k: int, router: Router, topk_ids, topk_weights, 
     T, E = logits.shape
     if token_mask is not None and token_mask.dtype == torch.bool:
         token_mask = token_mask.view(torch.uint8)
-    _check_err(err)
-    _call(lib().moe_route, "moe_route", dev, MoeShape(T, 8, E, 1, k), ctypes.byref(router), code,
+    _call(lib().moe_route, "moe_route", dev, _sizes(T, 8, E, k), ctypes.byref(router), code,
           _dev(logits, "logits", logits.dtype, (T, E), dev),
           _dev(bias, "bias", torch.float32, (E,), dev),
           _dev(token_mask, "token_mask", torch.uint8, (T,), dev),
           _dev(topk_ids, "topk_ids", torch.int32, (T, k), dev),
-          _dev(topk_weights, "topk_weights", torch.float32, (T, k), dev), _err_ptr(err, dev))
-
-
-def _err_ptr(err: torch.Tensor | None, device) -> int | None:
-    return None if err is None else _dev(err, "err", torch.int32, err.shape, device)
+          _dev(topk_weights, "topk_weights", torch.float32, (T, k), dev), _dev_err(err, dev))
 
 
 def route_backward(logits: torch.Tensor, topk_ids, router: Router, d_logits, *, d_weights=None,
@@ -688,17 +716,16 @@ def route_backward(logits: torch.Tensor, topk_ids, router: Router, d_logits, *, 
         counts = _dev(counts, "expert_counts", i32, (S, E), dev)
         tokens = _dev(tokens, "token_counts", i32, (S,), dev)
         offsets = _dev(offsets, "seq_offsets", i32, (S + 1,), dev)
-    _check_err(err)
-    _call(lib().moe_route_backward, "moe_route_backward", dev, MoeShape(T, 8, E, 1, k),
+    _call(lib().moe_route_backward, "moe_route_backward", dev, _sizes(T, 8, E, k),
           ctypes.byref(router), code, _dev(logits, "logits", logits.dtype, (T, E), dev),
           _dev(topk_ids, "topk_ids", i32, (T, k), dev),
           _dev(d_weights, "d_weights", f32, (T, k), dev), d_loss, counts, tokens, offsets, S,
-          _dev(d_logits, "d_logits", logits.dtype, (T, E), dev), _err_ptr(err, dev))
+          _dev(d_logits, "d_logits", logits.dtype, (T, E), dev), _dev_err(err, dev))
 
 
 def balance_workspace_bytes(T: int, E: int, k: int, sequences: int = 1) -> int:
     """moe_balance_workspace_bytes: scratch that balance_loss() needs."""
-    return int(lib().moe_balance_workspace_bytes(MoeShape(T, 8, E, 1, k), sequences))
+    return int(lib().moe_balance_workspace_bytes(_sizes(T, 8, E, k), sequences))
 
 
 def balance_loss(logits: torch.Tensor, topk_ids, router: Router, loss, expert_counts,
@@ -715,8 +742,7 @@ def balance_loss(logits: torch.Tensor, topk_ids, router: Router, loss, expert_co
         raise MoeError(f"topk_ids has shape {tuple(topk_ids.shape)}, the call needs [T, k]")
     k, S = topk_ids.shape[1], loss.numel()
     i32, f32 = torch.int32, torch.float32
-    _check_err(err)
-    _call(lib().moe_balance_loss, "moe_balance_loss", dev, MoeShape(T, 8, E, 1, k),
+    _call(lib().moe_balance_loss, "moe_balance_loss", dev, _sizes(T, 8, E, k),
           ctypes.byref(router), code, _dev(logits, "logits", logits.dtype, (T, E), dev),
           _dev(topk_ids, "topk_ids", i32, (T, k), dev),
           _dev(seq_offsets, "seq_offsets", i32, (S + 1,), dev), S,
@@ -725,7 +751,7 @@ def balance_loss(logits: torch.Tensor, topk_ids, router: Router, loss, expert_co
           _dev(token_counts, "token_counts", i32, (S,), dev),
           _dev(score_mean, "score_mean", f32, (S, E), dev),
           _dev(workspace, "workspace", workspace.dtype, workspace.shape, dev),
-          workspace.numel() * workspace.element_size(), _err_ptr(err, dev))
+          workspace.numel() * workspace.element_size(), _dev_err(err, dev))
 
 
 def expert_product(fmt: str, rows: torch.Tensor, expert_counts, expert_offsets, T: int, k: int,
@@ -750,17 +776,16 @@ def expert_product(fmt: str, rows: torch.Tensor, expert_counts, expert_offsets, 
     E, N, _ = w_q.shape
     code = ACTS[act]
     u8, i32 = torch.uint8, torch.int32
-    if rows.element_size() != 2 or out.element_size() != 2:
-        raise MoeError(f"expected 16-bit row tensors, got {rows.dtype} and {out.dtype}")
-    _check_err(err)
-    _call(lib().moe_expert_product, "moe_expert_product", dev, MoeShape(T, H, E, 1, k), N,
+    if rows.dtype not in ROW_TYPES or out.dtype not in ROW_TYPES:
+        raise MoeError(f"rows and out must be bf16 (or its bits), got {rows.dtype} and {out.dtype}")
+    _call(lib().moe_expert_product, "moe_expert_product", dev, _sizes(T, H, E, k), N,
           WIRE_CODES[fmt], code, _dev(rows, "rows", rows.dtype, (cap, H), dev),
           _dev(expert_counts, "expert_counts", i32, (E,), dev),
           _dev(expert_offsets, "expert_offsets", i32, (E + 1,), dev), cap,
           _dev(w_q, "w_q", u8, (E, N, H // 2), dev),
           _dev(w_scale, "w_scale", u8, (E, N, H // WIRE_FORMATS[fmt][1]), dev),
           _dev(factor, "factor", torch.float32, (E,), dev),
-          _dev(out, "out", out.dtype, (cap, N // 2 if code else N), dev), _err_ptr(err, dev))
+          _dev(out, "out", out.dtype, (cap, N // 2 if code else N), dev), _dev_err(err, dev))
 
 
 def time_next_launch(start: "torch.cuda.Event | None", stop: "torch.cuda.Event | None") -> None:

@@ -7,17 +7,18 @@
 //         Prefill and Decode"
 //
 // Kernels
-//  route_tokens    one wave per token: its logits in registers, k rounds of a
-//                  wave maximum for the choice, the weights ([A2A] sec 1.1:
-//                  the router picks k of the E experts and a weight for each)
-//  route_gradient  one wave per token: the gradient of its logits from the
-//                  weights' gradient and from the balance loss's
+//  route_tokens    four tokens per wave, 16 lanes each: the choice and the
+//                  weights ([A2A] sec 1.1: the router picks k of the E experts
+//                  and a weight for each); route_wide: one wave per token
+//  route_gradient  the gradient of the logits from the weights' gradient and
+//                  from the balance loss's
 //  balance_tiles   one workgroup per tile of tokens: the sums of the scores
 //                  and the pairs of each expert, sequence by sequence
-//  balance_join    one workgroup per sequence: joins the tiles' sums, the loss
-//                  ([EP]: the busiest GPU's experts set the time of a layer)
-// All of them read the logits once and are bound by that (and by the launch,
-// for a decode batch). Nothing depends on the order in which waves run.
+//  balance_join    one workgroup per (sequence, 64 experts): joins the tiles'
+//                  sums, the loss ([EP]: the busiest GPU's experts set the time
+//                  of a layer)
+// All of them read the logits once. No result depends on the order in which
+// waves run.
 
 #include "moe_common.h"
 
@@ -103,23 +104,43 @@ __device__ __forceinline__ void keep_groups(float (&key)[V], float* lds, int E, 
   __builtin_amdgcn_wave_barrier();
 }
 
-// One wave per token. Each of k rounds takes the wave's maximum (a lane's own
-// over its V registers, then 6 steps across lanes), finds its holders with a
-// ballot per register (the first set bit of the first register that has one is
-// the lowest expert id among equal keys) and strikes that one out.
+// The weights from the chosen logits: lane j of a row of 16 holds slot j's
+// (`mine`: it has an expert); `top` is the softmax's largest logit and `all` its
+// sum over all experts, used where the weights are not renormalised.
+// Sigmoids are taken times e^-m, m = min(0, largest chosen logit): none
+// underflows against another.
+template <bool kSigmoid>
+__device__ __forceinline__ float weight_of(const RouteArgs& a, bool mine, float zj, float top,
+                                           float all) {
+  float w = 0.0f, total = 1.0f;
+  if (kSigmoid) {
+    const float m = a.renorm ? fminf(0.0f, row_max(mine ? zj : -INFINITY)) : 0.0f;
+    if (mine) {
+      const float en = expf(-fabsf(zj));
+      w = zj >= 0.0f ? 1.0f / (1.0f + en) : expf(zj - m) / (1.0f + en);
+    }
+  } else {
+    if (mine) w = expf(zj - top);
+    total = all;
+  }
+  if (a.renorm) total = row_sum(w);
+  return mine ? w / total * a.scale : 0.0f;
+}
+
+// One wave for token t, every comparison exact. Each of k rounds takes the
+// wave's maximum (a lane's own over its V registers, then 6 steps across
+// lanes), finds its holders with a ballot per register (the first set bit of
+// the first register that has one is the lowest expert id among equal keys) and
+// strikes that one out.
 template <typename Tz, int V, bool kSigmoid, bool kKeyed>
-__global__ __launch_bounds__(kBlock) void route_tokens(RouteArgs a) {
-  extern __shared__ float lds_all[];
+__device__ __forceinline__ void route_exactly(const RouteArgs& a, int64_t t, float* lds) {
   const int lane = lane_id();
-  const int wave = wave_in_block();
-  const int64_t t = (int64_t)blockIdx.x * kWavesPerBlock + wave;
-  if (t >= a.T) return;
   const int E = a.E, k = a.k;
   bool routed = !a.mask || a.mask[t];
   float z[V], key[V];
-  int chosen = 0;      // experts found
-  int id = -1;         // lane j: the expert of slot j
-  float picked = 0.0f; // lane j: its key
+  int chosen = 0;       // experts found
+  int id = -1;          // lane j: the expert of slot j
+  float weight = 0.0f;  // and its weight
   const Tz* row = static_cast<const Tz*>(a.logits) + t * E;
   if (routed) {
     load_logits<Tz, V>(row, E, z);
@@ -140,10 +161,7 @@ __global__ __launch_bounds__(kBlock) void route_tokens(RouteArgs a) {
     }
   }
   if (routed) {
-    if (kKeyed && a.groups > 1)
-      keep_groups<V>(key, lds_all + wave * E, E, a.groups, a.top_groups);
-    float total = 0.0f;
-    float top = 0.0f;
+    if (kKeyed && a.groups > 1) keep_groups<V>(key, lds, E, a.groups, a.top_groups);
     for (int j = 0; j < k; ++j) {
       float m = key[0];
 #pragma unroll
@@ -164,41 +182,465 @@ __global__ __launch_bounds__(kBlock) void route_tokens(RouteArgs a) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (i == at && lane == win) key[i] = -INFINITY;
-      if (lane == j) {
-        id = at * kWave + win;
-        picked = m;
-      }
-      if (j == 0) top = m;
+      if (lane == j) id = at * kWave + win;
       ++chosen;
     }
     const bool mine = lane < chosen;
-    float w = 0.0f;
-    if (kSigmoid) {
-      // the scores times e^-m, m = min(0, largest chosen logit): no chosen
-      // score underflows against another
-      const float zj = kKeyed ? (mine ? float(row[id]) : -INFINITY) : (mine ? picked : -INFINITY);
-      const float m = a.renorm ? fminf(0.0f, row_max(zj)) : 0.0f;
-      if (mine) {
-        const float en = expf(-fabsf(zj));
-        w = zj >= 0.0f ? 1.0f / (1.0f + en) : expf(zj - m) / (1.0f + en);
-      }
-    } else {
-      if (mine) w = expf(picked - top);
+    const float zj = mine ? float(row[id]) : -INFINITY;
+    float top = 0.0f, all = 1.0f;
+    if (!kSigmoid) {
+      top = read_lane(row_max(zj), 0);
       if (!a.renorm) {
+        all = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) total += expf(z[i] - top);
-        total = wave_sum(total);
+        for (int i = 0; i < V; ++i) all += expf(z[i] - top);
+        all = wave_sum(all);
       }
     }
-    if (a.renorm) total = row_sum(w);
-    if (kSigmoid && !a.renorm) total = 1.0f;
-    picked = mine ? w / total * a.scale : 0.0f;
+    weight = weight_of<kSigmoid>(a, mine, zj, top, all);
   }
   if (lane < k) {
-    const bool mine = lane < chosen;
-    a.ids[t * k + lane] = mine ? id : -1;
-    a.weights[t * k + lane] = mine ? picked : 0.0f;
+    a.ids[t * k + lane] = lane < chosen ? id : -1;
+    a.weights[t * k + lane] = lane < chosen ? weight : 0.0f;
   }
+}
+
+// ---------------------------------------------------------------------------
+// Four tokens at a time
+
+// Whether a predicate holds in any lane of this lane's row of 16.
+__device__ __forceinline__ bool row_any(bool p) {
+  return ((__ballot(p) >> (lane_id() & 48)) & 0xFFFF) != 0;
+}
+
+// Rotations within a row (every lane has a source).
+template <int kCtrl>
+__device__ __forceinline__ int rotated(int v) {
+  return __builtin_amdgcn_mov_dpp(v, kCtrl, 0xF, 0xF, true);
+}
+
+__device__ __forceinline__ int row_max_int(int v) {
+  v = max(v, rotated<kRowRor + 8>(v));
+  v = max(v, rotated<kRowRor + 4>(v));
+  v = max(v, rotated<kRowRor + 2>(v));
+  return max(v, rotated<kRowRor + 1>(v));
+}
+
+// Of the lanes where p holds, the first of every row (p holds in each).
+__device__ __forceinline__ uint64_t first_of_rows(bool p) {
+  const uint64_t b = __ballot(p);
+  return b & ~(b - 0x0001000100010001ull);
+}
+
+// The two largest of a row, x >= y, from every lane's two.
+template <int kCtrl>
+__device__ __forceinline__ void merge_two(int& x, int& y) {
+  const int x2 = rotated<kCtrl>(x), y2 = rotated<kCtrl>(y);
+  y = max(min(x, x2), max(y, y2));
+  x = max(x, x2);
+}
+
+// Floats as integers of the same order (-0 as +0). Below kLeast lie -infinity
+// and kAbsent: no key.
+constexpr int kAbsent = INT32_MIN;
+constexpr int kLeast = int(0x80800000u);  // the lowest finite float
+__device__ __forceinline__ int ordered(float v) {
+  const int b = __float_as_int(v + 0.0f);
+  return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float unordered(int b) {
+  return __int_as_float(b ^ ((b >> 31) & 0x7FFFFFFF));
+}
+
+// Descending sort of n = 1, 2, 4, 8 or 16 integers in registers (Batcher's
+// odd-even merge sort).
+template <int N, int kLo, int kN>
+__device__ __forceinline__ void sort_run(int (&v)[N]) {
+  if constexpr (kN > 1) {
+    sort_run<N, kLo, kN / 2>(v);
+    sort_run<N, kLo + kN / 2, kN / 2>(v);
+#pragma unroll
+    for (int p = kN / 2; p >= 1; p /= 2) {
+      // p = kN / 2: halves against each other; then the inner pairs
+#pragma unroll
+      for (int i = 0; i < kN - p; ++i) {
+        const bool pair = p == kN / 2 ? i < p : i >= p && (i - p) % (2 * p) < p;
+        if (pair) {
+          const int x = v[kLo + i], y = v[kLo + i + p];
+          v[kLo + i] = max(x, y);
+          v[kLo + i + p] = min(x, y);
+        }
+      }
+    }
+  }
+}
+
+// A bitonic run of kN sorted, descending.
+template <int N, int kN>
+__device__ __forceinline__ void sort_bitonic(int (&v)[N]) {
+#pragma unroll
+  for (int p = kN / 2; p >= 1; p /= 2)
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if ((i & p) == 0) {
+        const int x = v[i], y = v[i + p];
+        v[i] = max(x, y);
+        v[i + p] = min(x, y);
+      }
+}
+
+// The L largest of V integers, descending, in v[0 .. L-1] (V a multiple of L):
+// runs of L sorted, then each merged into the first (the larger of the one and
+// the reverse of the other is bitonic and holds the L largest).
+template <int V, int L>
+__device__ __forceinline__ void largest(int (&v)[V]) {
+  sort_run<V, 0, L>(v);
+  if constexpr (V > L) {
+#pragma unroll
+    for (int r = L; r < V; r += L) {
+      int w[L];
+#pragma unroll
+      for (int i = 0; i < L; ++i) w[i] = v[r + i];
+      sort_run<L, 0, L>(w);
+#pragma unroll
+      for (int i = 0; i < L; ++i) v[i] = max(v[i], w[L - 1 - i]);
+      sort_bitonic<V, L>(v);
+    }
+  }
+}
+
+// Four tokens per wave, a row of 16 lanes each: expert e = 16 * i + l in
+// register i of the row's lane l. A key becomes an integer of the same order
+// whose kBits lowest bits hold V - 1 - i (of equal keys the lower register is
+// the larger integer); a lane keeps its L largest sorted, and each of k rounds
+// takes the row's largest head (4 steps within the row, for four tokens at
+// once), its first holder, and pops that lane's list. What the low bits have
+// hidden, and what a sigmoid in 32 bits may be off, can turn a choice only
+// where two keys next to each other in it (or a kept and a dropped group) are
+// that close. Then the candidates' exact keys (or the two groups') decide; what
+// even that leaves open (three as close) is chosen again by route_exactly.
+// Every vector step serves four tokens; with a wave per token the same work
+// took 28.2 us at T = 16384, E = 256, k = 8 with bias and 8 groups (float32
+// logits, 16.8 MB), this takes 14.0 us (16.6 with every close token chosen again).
+template <typename Tz, int V, int L, bool kSigmoid, bool kKeyed>
+__global__ __launch_bounds__(kBlock) void route_tokens(RouteArgs a) {
+  constexpr int kBits = V <= 2 ? 1 : V <= 4 ? 2 : V <= 8 ? 3 : V <= 16 ? 4 : 5;
+  constexpr int kLow = (1 << kBits) - 1;
+  constexpr bool kHidden = kKeyed || sizeof(Tz) == 4;  // low bits of a key can be lost
+  extern __shared__ float lds_all[];
+  const int lane = lane_id(), l = lane & 15;
+  const int wave = wave_in_block();
+  const int64_t first = ((int64_t)blockIdx.x * kWavesPerBlock + wave) * 4;
+  if (first >= a.T) return;
+  const int64_t t = first + (lane >> 4);
+  const int E = a.E, k = a.k;
+  bool routed = t < a.T && (!a.mask || a.mask[t]);
+  // loads of clamped places, all at once; what they hold past E or T or for a
+  // masked token is not used
+  const Tz* row = static_cast<const Tz*>(a.logits) + min(t, (int64_t)a.T - 1) * E;
+  Tz raw[V];
+  float bias[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) raw[i] = row[min(i * 16 + l, E - 1)];
+  if (kKeyed && a.bias) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) bias[i] = a.bias[min(i * 16 + l, E - 1)];
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) bias[i] = 0.0f;
+  }
+  float z[V];
+  int key[V];  // in the order of the keys
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    z[i] = routed && i * 16 + l < E ? float(raw[i]) : -INFINITY;
+    float v = z[i];
+    if (kKeyed) {
+      v = __builtin_amdgcn_rcpf(1.0f + __expf(-z[i])) + bias[i];
+      v = z[i] == -INFINITY ? -INFINITY : v;
+      bad |= !(v < INFINITY);
+    }
+    bad |= !(z[i] < INFINITY);
+    key[i] = ordered(v);
+  }
+  bool unsure = false;
+  if (row_any(bad)) {
+    if (l == 0) flag_error(a.err, MOE_ERRBIT_BAD_LOGIT);
+    routed = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = kAbsent;
+  }
+
+  if (kKeyed && a.groups > 1) {
+    // Group g is the registers [g * per, (g + 1) * per): the two largest keys of
+    // every group, its score in lane g of the row.
+    const int per = E / a.groups / 16;
+    int score_key = kAbsent;         // lane g: the group's score, as a key
+    int x = kAbsent, y = kAbsent;    // the two largest so far
+    int g = 0, left = per;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      y = max(y, min(x, key[i]));
+      x = max(x, key[i]);
+      if (--left == 0) {  // uniform
+        merge_two<kRowRor + 8>(x, y);
+        merge_two<kRowRor + 4>(x, y);
+        merge_two<kRowRor + 2>(x, y);
+        merge_two<kRowRor + 1>(x, y);
+        const int score = y >= kLeast ? ordered(unordered(x) + unordered(y)) : x;
+        if (l == g) score_key = score;
+        x = y = kAbsent;
+        ++g;
+        left = per;
+      }
+    }
+    int head = l < a.groups ? score_key : kAbsent;
+    // the best top_groups of them, the first of equal ones: lane g learns
+    // whether its group is kept, and all lanes the last kept and the first not
+    bool kept = false;
+    int worst = kAbsent;
+    uint64_t at_worst = 0;
+    for (int r = 0; r < a.top_groups; ++r) {
+      worst = row_max_int(head);
+      at_worst = first_of_rows(head == worst);
+      if (((at_worst >> lane) & 1) && head >= kLeast) {
+        kept = true;
+        head = kAbsent;
+      }
+    }
+    // a sigmoid here is off by at most 2^-22 (4 roundings), a score by twice that
+    // and its roundings, two scores by twice that
+    const int next = row_max_int(head);
+    const float slack = 2e-6f + fabsf(unordered(worst)) * 0x1p-21f;
+    const bool close = next >= kLeast && unordered(worst) - unordered(next) < slack;
+    if (__ballot(close && routed)) {
+      // exact scores of the two groups decide; a third as close goes the long way
+      const uint64_t at_next = first_of_rows(head == next);
+      const int group_a = __ffs(int(at_worst >> (lane & 48) & 0xFFFF)) - 1;
+      const int group_b = __ffs(int(at_next >> (lane & 48) & 0xFFFF)) - 1;
+      const int third = row_max_int(l == group_b ? kAbsent : head);
+      unsure |= close && third >= kLeast && unordered(worst) - unordered(third) < slack;
+      int before = l < a.groups && kept && l != group_a ? ordered(-unordered(score_key)) : kAbsent;
+      before = row_max_int(before);  // the last but one kept, negated
+      unsure |= close && before >= kLeast && -unordered(before) - unordered(next) < slack;
+      float score[2];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        int x2 = kAbsent, y2 = kAbsent;
+        for (int i = 0; i < per; ++i) {
+          const int e = min((w ? group_b : group_a) * per * 16 + i * 16 + l, E - 1);
+          const float ze = float(row[e]);
+          const float ke = sigmoid_nearest(ze) + (a.bias ? a.bias[e] : 0.0f);
+          const int o = ze == -INFINITY ? kAbsent : ordered(ke);
+          y2 = max(y2, min(x2, o));
+          x2 = max(x2, o);
+        }
+        merge_two<kRowRor + 8>(x2, y2);
+        merge_two<kRowRor + 4>(x2, y2);
+        merge_two<kRowRor + 2>(x2, y2);
+        merge_two<kRowRor + 1>(x2, y2);
+        score[w] = y2 >= kLeast ? unordered(x2) + unordered(y2) : unordered(x2);
+      }
+      const bool swap = score[1] > score[0] || (score[1] == score[0] && group_b < group_a);
+      if (close && swap) kept = l == group_b || (kept && l != group_a);
+    }
+    const uint32_t keep = uint32_t(__ballot(kept) >> (lane & 48));
+    uint32_t bit = 1;
+    left = per;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      key[i] = keep & bit ? key[i] : kAbsent;
+      if (--left == 0) {
+        bit <<= 1;
+        left = per;
+      }
+    }
+  }
+
+  int list[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    list[i] = (key[i] & ~kLow) | (V - 1 - i);
+  largest<V, L>(list);
+  const bool full = V > L && list[L - 1] >= kLeast;
+  // One candidate more than slots (where the row has a lane for it): the choice
+  // is put right among them below.
+  const int taken = kHidden ? min(k + 1, 16) : k;
+  int found = kAbsent;          // lane j: candidate j's key
+  uint32_t low0 = 0, low1 = 0;  // and the lanes its round took it from
+  for (int j = 0; j < taken; ++j) {
+    const int m = row_max_int(list[0]);
+    const uint64_t low = first_of_rows(list[0] == m);
+    if (l == j) {
+      found = m;
+      low0 = uint32_t(low);
+      low1 = uint32_t(low >> 32);
+    }
+    if ((low >> lane) & 1) {
+#pragma unroll
+      for (int i = 0; i + 1 < L; ++i) list[i] = list[i + 1];
+      list[L - 1] = kAbsent;
+    }
+  }
+  const bool candidate = l < taken && found >= kLeast;
+  const uint32_t field = (lane & 32 ? low1 : low0) >> (lane & 16) & 0xFFFF;
+  const int id = candidate ? (V - 1 - (found & kLow)) * 16 + __ffs(int(field)) - 1 : -1;
+  float zj = candidate ? float(row[id]) : -INFINITY;
+  int slot = l;
+  if (kHidden) {
+    // Whether a candidate may come before one whose key is `after` at most.
+    auto close = [&](int after) {
+      if (after < kLeast) return false;
+      if (!kKeyed) return (found | kLow) == (after | kLow);
+      const float v = unordered(found | kLow);
+      return v - unordered(after & ~kLow) < 1e-6f + fabsf(v) * (0x1p-22f + 0x1p-22f * kLow);
+    };
+    const int rest = row_max_int(list[0]);
+    const int shifted = __builtin_amdgcn_update_dpp(kAbsent, found, 0x101, 0xF, 0xF, false);
+    const bool near = candidate && l < k && close(l == taken - 1 ? rest : shifted);
+    // what is not among the candidates may be the last slot's, or be hidden
+    // behind a list that has run out: the long way
+    unsure |= candidate && l == k - 1 && close(rest);
+    unsure |= full && list[0] < kLeast;
+    if (__ballot(near && routed)) {
+      // the candidates' exact keys, and each one's place by them
+      float exact = zj;
+      if (kKeyed && candidate) exact = sigmoid_nearest(zj) + (a.bias ? a.bias[id] : 0.0f);
+      if (!candidate) exact = -INFINITY;
+      slot = 0;
+#pragma unroll
+      for (int r = 1; r < 16; ++r) {
+        // the candidate r lanes on
+        const int from = (lane & 48) | ((l + r) & 15);
+        const float other = __shfl(exact, from);
+        const int other_id = __shfl(id, from);
+        slot += other > exact || (other == exact && other_id >= 0 && other_id < id) ? 1 : 0;
+      }
+      if (!candidate) slot = 16;
+    }
+  }
+  const bool mine = candidate && slot < k;
+  if (!mine) zj = -INFINITY;
+
+  float top = 0.0f, all = 1.0f;
+  if (!kSigmoid) {
+    top = row_max(zj);
+    if (!a.renorm) {
+      all = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) all += expf(z[i] - top);
+      all = row_sum(all);
+    }
+  }
+  const float weight = weight_of<kSigmoid>(a, mine, zj, top, all);
+  const uint64_t again = kHidden ? __ballot(unsure && routed) : 0;
+  if (t < a.T && !((again >> (lane & 48)) & 0xFFFF)) {
+    // slots that no candidate takes are the last ones
+    const int count = __popc(uint32_t(__ballot(mine) >> (lane & 48)) & 0xFFFF);
+    const int to = mine ? slot : l;
+    if (mine || (l >= count && l < k)) {
+      a.ids[t * k + to] = mine ? id : -1;
+      a.weights[t * k + to] = weight;
+    }
+  }
+  if (kHidden) {
+    if (again) {
+      constexpr int V64 = (V + 3) / 4;
+#pragma unroll 1
+      for (int r = 0; r < 4; ++r)
+        if ((again >> (16 * r)) & 0xFFFF)
+          route_exactly<Tz, V64, kSigmoid, kKeyed>(a, first + r, lds_all + wave * E);
+    }
+  }
+}
+
+// One wave per token, for what route_tokens does not take: more than 512
+// experts, or groups that do not fill rows of 16 experts.
+template <typename Tz, int V, bool kSigmoid, bool kKeyed>
+__global__ __launch_bounds__(kBlock) void route_wide(RouteArgs a) {
+  extern __shared__ float lds_all[];
+  const int wave = wave_in_block();
+  const int64_t t = (int64_t)blockIdx.x * kWavesPerBlock + wave;
+  if (t < a.T) route_exactly<Tz, V, kSigmoid, kKeyed>(a, t, lds_all + wave * a.E);
+}
+
+// ---------------------------------------------------------------------------
+// Scores of whole tokens (the balance loss, the gradient)
+
+// LT lanes per token: 16 (four tokens a wave) up to 512 experts, 64 above.
+// Expert e = LT * i + l lies in register i of the token's lane l.
+template <int LT>
+__device__ __forceinline__ float token_sum(float v) {
+  return LT == 16 ? row_sum(v) : wave_sum(v);
+}
+template <int LT>
+__device__ __forceinline__ float token_max(float v) {
+  return LT == 16 ? row_max(v) : wave_max(v);
+}
+template <int LT>
+__device__ __forceinline__ bool token_any(bool p) {
+  return LT == 16 ? row_any(p) : __ballot(p) != 0;
+}
+
+// e^x for x <= 88 to about 1.5 roundings: 2^(x log2 e) with the product's
+// rounding put right; below e^-104 it is 0.
+__device__ __forceinline__ float exp_near(float x) {
+  constexpr float kLog2e = 1.44269504089f, kLn2 = 0.693147180560f;
+  x = __builtin_amdgcn_fmed3f(x, -104.0f, 88.0f);
+  const float h = x * kLog2e;
+  const float rest = fmaf(x, kLog2e, -h) + x * 1.925963033e-8f;  // log2 e beyond its float
+  const float r = __builtin_amdgcn_exp2f(h);
+  return fmaf(r, rest * kLn2, r);
+}
+
+// A token's scores scaled to a sum of one (p), and for sigmoid 1 - s of each
+// (inner). Masked experts, and those past E, have -infinity and get 0.
+template <int LT, int V, bool kSigmoid>
+__device__ __forceinline__ void shares(const float (&z)[V], float (&p)[V], float (&inner)[V]) {
+  float m = z[0];
+#pragma unroll
+  for (int i = 1; i < V; ++i) m = fmaxf(m, z[i]);
+  m = token_max<LT>(m);
+  if (m == -INFINITY) m = 0.0f;  // no expert has a score: all shares are 0
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (kSigmoid) {
+      const float en = exp_near(-z[i]);
+      p[i] = __builtin_amdgcn_rcpf(1.0f + en);
+      inner[i] = en * p[i];
+    } else {
+      p[i] = exp_near(z[i] - m);
+    }
+    p[i] = z[i] == -INFINITY ? 0.0f : p[i];
+  }
+  if (kSigmoid && __ballot(m < -40.0f)) {
+    // all sigmoids of some token are tiny: there they are taken times e^-m
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (m < -40.0f) {
+        p[i] = z[i] == -INFINITY ? 0.0f : exp_near(z[i] - m);  // 1 + e^z is 1
+        inner[i] = 1.0f;
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) sum += p[i];
+  sum = token_sum<LT>(sum);
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) p[i] *= inv;
+}
+
+// The logits of a token with E experts; -infinity where it takes no part.
+template <typename Tz, int LT, int V>
+__device__ __forceinline__ void token_logits(const Tz* row, int l, int E, bool used,
+                                             float (&z)[V]) {
+  Tz raw[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) raw[i] = row[min(i * LT + l, E - 1)];  // all at once
+#pragma unroll
+  for (int i = 0; i < V; ++i) z[i] = used && i * LT + l < E ? float(raw[i]) : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
@@ -222,9 +664,11 @@ struct BalanceArgs {
   const void* logits;
   const int32_t* ids;
   const int32_t* offsets;  // NULL: one sequence of all tokens
-  float* sums;             // [(tiles + S) * E] sums of the scores
-  int32_t* pairs;          // [(tiles + S) * E] pairs
-  int32_t* used;           // [tiles + S] tokens with an expert
+  float* sums;             // [slots * E] sums of the scores, slots = tiles + S
+  int32_t* pairs;          // [slots * E] pairs
+  int32_t* used;           // [slots] tokens with an expert
+  double* terms;           // [S * columns] parts of the loss
+  uint32_t* done;          // [S] columns that are joined
   float* loss;
   int32_t* counts;
   int32_t* tokens;
@@ -233,60 +677,31 @@ struct BalanceArgs {
   int T, E, k, S, tile;
 };
 
-// A token's scores scaled to a sum of one: softmax, or sigmoid over the sum
-// of sigmoids (times e^-m as in route_tokens). Experts past E give 0.
-template <int V, bool kSigmoid>
-__device__ __forceinline__ void shares(const float (&z)[V], float (&p)[V]) {
-  float m = z[0];
-#pragma unroll
-  for (int i = 1; i < V; ++i) m = fmaxf(m, z[i]);
-  m = wave_max(m);
-  if (kSigmoid) m = fminf(m, 0.0f);
-  if (m == -INFINITY) m = 0.0f;  // no expert has a score: all shares are 0
-  float sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if (kSigmoid) {
-      const float en = expf(-fabsf(z[i]));
-      p[i] = (z[i] >= 0.0f ? 1.0f : expf(z[i] - m)) / (1.0f + en);
-    } else {
-      p[i] = expf(z[i] - m);
-    }
-    sum += p[i];
-  }
-  sum = wave_sum(sum);
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) p[i] *= inv;
-}
-
-constexpr int kTileThreads = 1024;
+constexpr int kTileThreads = 512;
 constexpr int kTileWaves = kTileThreads / kWave;
+constexpr int kColumn = 64;  // experts that a workgroup joins
 
-// Whether a wave's token has an expert; counts its pairs in LDS.
-__device__ __forceinline__ bool token_used(const BalanceArgs& a, int64_t t, int* pairs) {
-  const int lane = lane_id();
-  const int id = lane < a.k ? a.ids[t * a.k + lane] : -1;
-  const bool ok = id >= 0 && id < a.E;
-  if (__ballot(id < -1 || id >= a.E) && lane == 0) flag_error(a.err, MOE_ERRBIT_BAD_ID);
-  if (ok) atomicAdd(pairs + id, 1);  // integers: any order gives the same count
-  return __ballot(ok) != 0;
-}
-
-// One workgroup per tile of tokens, one wave per token in turn; the scores are
-// summed per lane in registers. Where a sequence ends within the tile, the
-// sums so far go to the slot tile + sequence (increasing along the tokens, so
-// no two pairs of them share one) and start anew.
-template <typename Tz, int V, bool kSigmoid>
+// One workgroup per tile of tokens, each wave 64 / LT tokens at a time; the
+// scores are summed per lane in registers. Where a sequence ends within the
+// tile, the sums so far go to the slot tile + sequence (increasing along the
+// tokens, so no two pairs of them share one) and start anew. Bound by
+// latency: T = 16384, E = 256 with sigmoids of bfloat16 logits (8.4 MB) takes
+// XX us; with a wave per token it was 23.7 us.
+template <typename Tz, int LT, int V, bool kSigmoid>
 __global__ __launch_bounds__(kTileThreads) void balance_tiles(BalanceArgs a) {
   extern __shared__ float lds_all[];
   const int E = a.E;
   int* pairs = reinterpret_cast<int*>(lds_all);  // [E]
   int* used = pairs + E;                         // [1]
-  float* part = lds_all + E + 1;                 // [waves / 2 * E]
-  const int wave = wave_in_block(), lane = lane_id();
+  float* part = lds_all + E + 1;                 // [waves * E]
+  constexpr int kTokens = kWave / LT;
+  const int wave = wave_in_block(), lane = lane_id(), l = lane % LT;
   const int64_t begin = (int64_t)blockIdx.x * a.tile;
   const int64_t end = min(begin + a.tile, (int64_t)a.T);
+  // the joining workgroups' counts start at 0 (this kernel runs before them)
+  for (int64_t i = (int64_t)blockIdx.x * kTileThreads + threadIdx.x; i < a.S;
+       i += (int64_t)gridDim.x * kTileThreads)
+    a.done[i] = 0;
   int s = a.offsets ? sequence_of(a.offsets, a.S, begin) : 0;
   for (; s < a.S; ++s) {
     const int64_t first = a.offsets ? max((int64_t)a.offsets[s], begin) : begin;
@@ -298,36 +713,37 @@ __global__ __launch_bounds__(kTileThreads) void balance_tiles(BalanceArgs a) {
     float sum[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) sum[i] = 0.0f;
-    int n = 0;
-    for (int64_t t = first + wave; t < last; t += kTileWaves) {
-      if (!token_used(a, t, pairs)) continue;
-      ++n;
-      float z[V], p[V];
-      load_logits<Tz, V>(static_cast<const Tz*>(a.logits) + t * E, E, z);
-      shares<V, kSigmoid>(z, p);
+    for (int64_t t0 = first + wave * kTokens; t0 < last; t0 += kTileWaves * kTokens) {
+      const int64_t t = t0 + lane / LT;
+      const bool here = t < last;
+      const int64_t at = min(t, last - 1);
+      const int id = here && l < a.k ? a.ids[at * a.k + l] : -1;
+      float z[V], p[V], inner[V];
+      const bool ok = id >= 0 && id < E;
+      if (__ballot(id < -1 || id >= E) && lane == 0) flag_error(a.err, MOE_ERRBIT_BAD_ID);
+      if (ok) atomicAdd(pairs + id, 1);  // integers: any order gives the same count
+      const bool counted = token_any<LT>(ok);
+      if (counted && l == 0) atomicAdd(used, 1);
+      token_logits<Tz, LT, V>(static_cast<const Tz*>(a.logits) + at * E, l, E, counted, z);
+      shares<LT, V, kSigmoid>(z, p, inner);
 #pragma unroll
       for (int i = 0; i < V; ++i) sum[i] += p[i];
     }
-    if (lane == 0 && n) atomicAdd(used, n);
-    // the upper half of the waves hands its sums to the lower half, whose
-    // are then added up in wave order (half the LDS of all of them at once)
-    constexpr int kHalf = kTileWaves / 2;
-    if (wave >= kHalf) {
+    // the wave's tokens together, then the waves in order
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i * kWave + lane < E) part[(wave - kHalf) * E + i * kWave + lane] = sum[i];
-    }
-    __syncthreads();
-    if (wave < kHalf) {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i * kWave + lane < E) part[wave * E + i * kWave + lane] += sum[i];
+    for (int i = 0; i < V; ++i) {
+      if (LT == 16) {
+        sum[i] += __shfl_xor(sum[i], 16);
+        sum[i] += __shfl_xor(sum[i], 32);
+      }
+      if (lane < LT && i * LT + l < E) part[wave * E + i * LT + l] = sum[i];
     }
     __syncthreads();
     const int64_t slot = (int64_t)blockIdx.x + s;
     for (int e = threadIdx.x; e < E; e += kTileThreads) {
       float total = 0.0f;
-      for (int w = 0; w < kHalf; ++w) total += part[w * E + e];
+#pragma unroll
+      for (int w = 0; w < kTileWaves; ++w) total += part[w * E + e];
       a.sums[slot * E + e] = total;
       a.pairs[slot * E + e] = pairs[e];
     }
@@ -336,13 +752,17 @@ __global__ __launch_bounds__(kTileThreads) void balance_tiles(BalanceArgs a) {
   }
 }
 
-// One workgroup per sequence. The tiles' sums of a column are added in tile
-// order, in 64 bits, by as many threads as there are columns times slices.
-__global__ __launch_bounds__(kTileThreads) void balance_join(BalanceArgs a) {
-  __shared__ double lds_sum[kTileThreads];
-  __shared__ int lds_pairs[kTileThreads];
+// One workgroup per (sequence, 64 experts). The tiles' sums of an expert are
+// added by 16 threads, in an order that the sizes alone fix, in 64 bits. The
+// workgroup that finishes a sequence last adds up the loss's parts, in order.
+__global__ __launch_bounds__(1024) void balance_join(BalanceArgs a) {
+  constexpr int kSlices = 1024 / kColumn;
+  __shared__ double lds_sum[1024];
+  __shared__ int lds_pairs[1024];
   __shared__ int lds_used;
-  const int E = a.E, s = blockIdx.x, tid = threadIdx.x;
+  __shared__ bool lds_last;
+  const int E = a.E, columns = (E + kColumn - 1) / kColumn;
+  const int s = blockIdx.x / columns, column = blockIdx.x % columns, tid = threadIdx.x;
   int64_t first = a.offsets ? a.offsets[s] : 0, last = a.offsets ? a.offsets[s + 1] : a.T;
   if (first < 0 || last > a.T || first > last) {
     if (tid == 0) flag_error(a.err, MOE_ERRBIT_BAD_SEQ);
@@ -352,41 +772,49 @@ __global__ __launch_bounds__(kTileThreads) void balance_join(BalanceArgs a) {
   const int64_t w1 = last > first ? (last - 1) / a.tile + 1 : w0;
   if (tid == 0) lds_used = 0;
   __syncthreads();
-  for (int64_t w = w0 + tid; w < w1; w += kTileThreads) atomicAdd(&lds_used, a.used[w + s]);
-  const int slices = kTileThreads / E;  // E <= 1024
-  const int e = tid % E, slice = tid / E;
+  int n = 0;
+  for (int64_t w = w0 + tid; w < w1; w += 1024) n += a.used[w + s];
+  if (n) atomicAdd(&lds_used, n);
+  const int e = column * kColumn + tid % kColumn, slice = tid / kColumn;
   double sum = 0.0;
   int pairs = 0;
-  if (slice < slices)
-    for (int64_t w = w0 + slice; w < w1; w += slices) {
+  if (e < E) {
+#pragma unroll 4
+    for (int64_t w = w0 + slice; w < w1; w += kSlices) {
       sum += a.sums[(w + s) * E + e];
       pairs += a.pairs[(w + s) * E + e];
     }
+  }
   lds_sum[tid] = sum;
   lds_pairs[tid] = pairs;
   __syncthreads();
-  const int n = lds_used;
-  double term = 0.0;
-  if (tid < E) {
-    for (int q = 1; q < slices; ++q) {
-      sum += lds_sum[q * E + e];
-      pairs += lds_pairs[q * E + e];
+  n = lds_used;
+  if (tid < kColumn) {
+    for (int q = 1; q < kSlices; ++q) {
+      sum += lds_sum[q * kColumn + tid];
+      pairs += lds_pairs[q * kColumn + tid];
     }
     const double mean = n > 0 ? sum / n : 0.0;
-    a.counts[(int64_t)s * E + e] = pairs;
-    a.mean[(int64_t)s * E + e] = float(mean);
-    term = mean * pairs;
-  }
-  __syncthreads();
-  lds_sum[tid] = term;
-  __syncthreads();
-  for (int h = kTileThreads / 2; h > 0; h >>= 1) {
-    if (tid < h) lds_sum[tid] += lds_sum[tid + h];
-    __syncthreads();
-  }
-  if (tid == 0) {
-    a.tokens[s] = n;
-    a.loss[s] = n > 0 ? float(lds_sum[0] * E / (double(a.k) * n)) : 0.0f;
+    if (e < E) {
+      a.counts[(int64_t)s * E + e] = pairs;
+      a.mean[(int64_t)s * E + e] = float(mean);
+    }
+    double term = mean * pairs;  // the wave's 64 experts, by halves
+    for (int h = kColumn / 2; h > 0; h >>= 1) term += __shfl_xor(term, h);
+    if (tid == 0) {
+      a.terms[(int64_t)s * columns + column] = term;
+      __threadfence();
+      lds_last = atomicAdd(a.done + s, 1u) + 1 == uint32_t(columns);
+      if (lds_last) {
+        __threadfence();
+        double total = 0.0;
+        for (int c = 0; c < columns; ++c)
+          total += __hip_atomic_load(a.terms + (int64_t)s * columns + c, __ATOMIC_RELAXED,
+                                     __HIP_MEMORY_SCOPE_AGENT);
+        a.tokens[s] = n;
+        a.loss[s] = n > 0 ? float(total * E / (double(a.k) * n)) : 0.0f;
+      }
+    }
   }
 }
 
@@ -416,107 +844,127 @@ struct GradArgs {
 // For the balance loss u_e = d E n_e / (k T'^2). One number taken off every u
 // changes nothing in u_e - sum p u, so k T' / E is taken off n_e first: what
 // is left to cancel is the imbalance, not the counts.
-template <typename Tz, int V, bool kSigmoid>
+// The slots' parts reach their experts' lanes through LDS. Bound by the bytes:
+// T = 16384, E = 256 in float32 (33.6 MB both ways) takes XX us, 13.8 us
+// with a wave per token.
+template <typename Tz, int LT, int V, bool kSigmoid>
 __global__ __launch_bounds__(kBlock) void route_gradient(GradArgs a) {
-  const int lane = lane_id();
-  const int64_t t = (int64_t)blockIdx.x * kWavesPerBlock + wave_in_block();
-  if (t >= a.T) return;
+  constexpr int kTokens = kWave / LT;
+  extern __shared__ float lds_all[];
+  const int lane = lane_id(), l = lane % LT, wave = wave_in_block();
+  const int64_t t0 = ((int64_t)blockIdx.x * kWavesPerBlock + wave) * kTokens;
+  if (t0 >= a.T) return;
   const int E = a.E, k = a.k;
-  const Tz* row = static_cast<const Tz*>(a.logits) + t * E;
-  Tz* out = static_cast<Tz*>(a.d_logits) + t * E;
-  const int id = lane < k ? a.ids[t * k + lane] : -1;
+  float* spread = lds_all + (wave * kTokens + lane / LT) * E;  // this token's experts
+  const int64_t t = t0 + lane / LT;
+  const bool here = t < a.T;
+  const int64_t at = min(t, (int64_t)a.T - 1);
+  const Tz* row = static_cast<const Tz*>(a.logits) + at * E;
+  const int id = here && l < k ? a.ids[at * k + l] : -1;
   const bool ok = id >= 0 && id < E;
   if (__ballot(id < -1 || id >= E) && lane == 0) flag_error(a.err, MOE_ERRBIT_BAD_ID);
-  const bool used = __ballot(ok) != 0;
-  float d[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) d[i] = 0.0f;
+  const bool used = token_any<LT>(ok);
   int s = 0;
   bool inside = used && a.d_loss;
-  if (inside && a.offsets) {
-    s = sequence_of(a.offsets, a.S, t);
-    inside = s < a.S && a.offsets[s] <= t;
+  if (a.d_loss && a.offsets) {
+    s = sequence_of(a.offsets, a.S, at);
+    inside = inside && s < a.S && a.offsets[min(s, a.S - 1)] <= t;
+    s = min(s, a.S - 1);
   }
-  if (used) {
-    float z[V];
-    load_logits<Tz, V>(row, E, z);
-    const float g = ok && a.d_weights ? a.d_weights[t * k + lane] * a.scale : 0.0f;
-    const bool dense = !kSigmoid && !a.renorm && a.d_weights;
-    float part = 0.0f;  // lane j: what slot j adds to its expert
-    if (a.d_weights) {
-      const float zj = ok ? float(row[id]) : -INFINITY;
-      float q = 0.0f;
-      if (kSigmoid) {
-        const float m = a.renorm ? fminf(0.0f, row_max(zj)) : 0.0f;
-        const float en = expf(-fabsf(zj));
-        if (zj > -INFINITY) q = (zj >= 0.0f ? 1.0f : expf(zj - m)) / (1.0f + en);
-        if (a.renorm) {
-          const float sum = row_sum(q);
-          q = sum > 0.0f ? q / sum : 0.0f;
-        }
-        const float inner = (zj >= 0.0f ? en : 1.0f) / (1.0f + en);
-        part = inner * q * (g - (a.renorm ? row_sum(q * g) : 0.0f));
-      } else if (a.renorm) {
-        const float m = row_max(zj);
-        if (ok && m > -INFINITY) q = expf(zj - m);
+  float z[V], d[V], u[V];
+  token_logits<Tz, LT, V>(row, l, E, used, z);
+#pragma unroll
+  for (int i = 0; i < V; ++i) d[i] = u[i] = 0.0f;
+  const bool dense = !kSigmoid && !a.renorm && a.d_weights;
+
+  if (a.d_weights) {
+    const float g = ok ? a.d_weights[at * k + l] * a.scale : 0.0f;
+    const float zj = ok ? float(row[id]) : -INFINITY;
+    float q = 0.0f, part = g;  // part: what slot l adds to its expert
+    if (kSigmoid) {
+      const float m = a.renorm ? fminf(0.0f, row_max(zj)) : 0.0f;
+      const float en = expf(-fabsf(zj));
+      if (zj > -INFINITY) q = (zj >= 0.0f ? 1.0f : expf(zj - m)) / (1.0f + en);
+      if (a.renorm) {
         const float sum = row_sum(q);
         q = sum > 0.0f ? q / sum : 0.0f;
-        part = q * (g - row_sum(q * g));
-      } else {
-        part = g;
       }
-      if (!ok) part = 0.0f;
+      const float away = (zj >= 0.0f ? en : 1.0f) / (1.0f + en);
+      part = away * q * (g - (a.renorm ? row_sum(q * g) : 0.0f));
+    } else if (a.renorm) {
+      const float m = row_max(zj);
+      if (ok && m > -INFINITY) q = expf(zj - m);
+      const float sum = row_sum(q);
+      q = sum > 0.0f ? q / sum : 0.0f;
+      part = q * (g - row_sum(q * g));
     }
-    float u[V];
+    // To the experts' lanes. The slot that finds another's number in its
+    // expert's place shares it: then the slots add one after the other.
 #pragma unroll
-    for (int i = 0; i < V; ++i) u[i] = 0.0f;
-    if (a.d_weights) {
+    for (int i = 0; i < V; ++i)
+      if (i * LT + l < E) spread[i * LT + l] = 0.0f;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (ok) spread[id] = float(l);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const bool shared = ok && spread[id] != float(l);
+    const bool again = __ballot(shared) != 0;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (!again) {
+      if (ok) spread[id] = part;
+    } else {
+      if (ok) spread[id] = 0.0f;
       for (int j = 0; j < k; ++j) {
-        const int e = read_lane(id, j);
-        const float v = read_lane(part, j);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (i * kWave + lane == e) u[i] += v;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (ok && l == j) spread[id] += part;
       }
     }
-    if (!dense) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        d[i] = u[i];
-        u[i] = 0.0f;
-      }
-    }
-    if (inside) {
-      const int n = a.tokens[s];
-      const float rate =
-          n > 0 ? float(double(a.d_loss[s]) * E / (double(k) * double(n) * double(n))) : 0.0f;
-      const float off = float(double(k) * n / E);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = i * kWave + lane;
-        if (e < E) u[i] += rate * (float(a.counts[(int64_t)s * E + e]) - off);
-      }
-    }
-    if (dense || inside) {
-      float p[V];
-      shares<V, kSigmoid>(z, p);
-      float dot = 0.0f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) dot += p[i] * u[i];
-      dot = wave_sum(dot);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float v = p[i] * (u[i] - dot);
-        if (kSigmoid) v *= 1.0f / (1.0f + expf(z[i]));
-        d[i] += v;
-      }
+    for (int i = 0; i < V; ++i) {
+      const float v = i * LT + l < E ? spread[i * LT + l] : 0.0f;
+      if (dense)
+        u[i] = v;
+      else
+        d[i] = v;
     }
   }
+
+  if (a.d_loss) {
+    const int n = a.tokens[s];
+    const float rate = inside && n > 0 ? float(double(a.d_loss[s]) * E /
+                                               (double(k) * double(n) * double(n)))
+                                       : 0.0f;
+    const float off = float(double(k) * n / E);
+    int count[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = i * kWave + lane;
-    if (e < E) out[e] = Tz(d[i]);
+    for (int i = 0; i < V; ++i) count[i] = a.counts[(int64_t)s * E + min(i * LT + l, E - 1)];
+#pragma unroll
+    for (int i = 0; i < V; ++i) u[i] += rate * (float(count[i]) - off);
   }
+  if (dense || a.d_loss) {
+    float p[V], inner[V];
+    shares<LT, V, kSigmoid>(z, p, inner);
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) dot += p[i] * u[i];
+    dot = token_sum<LT>(dot);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float v = p[i] * (u[i] - dot);
+      if (kSigmoid) v *= inner[i];
+      d[i] += used && p[i] != 0.0f ? v : 0.0f;
+    }
+  }
+  if (!here) return;
+  Tz* out = static_cast<Tz*>(a.d_logits) + t * E;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i * LT + l < E) out[i * LT + l] = Tz(d[i]);
 }
 
 // ---------------------------------------------------------------------------
@@ -536,7 +984,7 @@ bool router_ok(const moe_shape_t* sh, const moe_router_t* r, int type) {
   return true;
 }
 
-// Calls fn<Tz, V>: V registers of 64 experts each.
+// Calls F<Tz, V>::go: V registers of 64 experts each.
 template <template <typename, int> class F, typename Tz, typename... Args>
 void by_experts(int E, Args&&... args) {
   const int v = (E + kWave - 1) / kWave;
@@ -557,52 +1005,125 @@ void by_type(int type, int E, Args&&... args) {
 
 int token_blocks(int T) { return (T + kWavesPerBlock - 1) / kWavesPerBlock; }
 
+bool keyed(const RouteArgs& a, int scoring) {
+  return scoring == MOE_SCORE_SIGMOID && (a.bias || a.groups > 1);
+}
+
+// LDS of the exact choice: its groups' keys.
+size_t route_lds(const RouteArgs& a) {
+  return a.groups > 1 ? size_t(kWavesPerBlock) * a.E * 4 : 0;
+}
+
 template <typename Tz, int V>
-struct RouteLaunch {
+struct RouteWideLaunch {
   static void go(hipStream_t st, const RouteArgs& a, int scoring) {
     const dim3 grid(token_blocks(a.T));
-    const bool keyed = scoring == MOE_SCORE_SIGMOID && (a.bias || a.groups > 1);
-    const size_t lds = a.groups > 1 ? size_t(kWavesPerBlock) * a.E * 4 : 0;
-    if (keyed)
-      route_tokens<Tz, V, true, true><<<grid, kBlock, lds, st>>>(a);
+    if (keyed(a, scoring))
+      route_wide<Tz, V, true, true><<<grid, kBlock, route_lds(a), st>>>(a);
     else if (scoring == MOE_SCORE_SIGMOID)
-      route_tokens<Tz, V, true, false><<<grid, kBlock, 0, st>>>(a);
+      route_wide<Tz, V, true, false><<<grid, kBlock, 0, st>>>(a);
     else
-      route_tokens<Tz, V, false, false><<<grid, kBlock, 0, st>>>(a);
+      route_wide<Tz, V, false, false><<<grid, kBlock, 0, st>>>(a);
   }
 };
 
-template <typename Tz, int V>
+template <typename Tz, int V, int L>
+void launch_route(hipStream_t st, const RouteArgs& a, int scoring) {
+  const dim3 grid((token_blocks(a.T) + 3) / 4);
+  if (keyed(a, scoring))
+    route_tokens<Tz, V, L, true, true><<<grid, kBlock, route_lds(a), st>>>(a);
+  else if (scoring == MOE_SCORE_SIGMOID)
+    route_tokens<Tz, V, L, true, false><<<grid, kBlock, 0, st>>>(a);
+  else
+    route_tokens<Tz, V, L, false, false><<<grid, kBlock, 0, st>>>(a);
+}
+
+template <typename Tz>
+struct RouteLaunch {
+  static void go(hipStream_t st, const RouteArgs& a, int scoring) {
+    const int v = (a.E + 15) / 16;
+    if (v <= 4) return launch_route<Tz, 4, 4>(st, a, scoring);
+    if (a.k <= 8) {
+      if (v <= 8) return launch_route<Tz, 8, 8>(st, a, scoring);
+      if (v <= 16) return launch_route<Tz, 16, 8>(st, a, scoring);
+      if (v <= 24) return launch_route<Tz, 24, 8>(st, a, scoring);
+      return launch_route<Tz, 32, 8>(st, a, scoring);
+    }
+    if (v <= 8) return launch_route<Tz, 8, 8>(st, a, scoring);
+    if (v <= 16) return launch_route<Tz, 16, 16>(st, a, scoring);
+    return launch_route<Tz, 32, 16>(st, a, scoring);
+  }
+};
+
+template <typename Tz, int LT, int V>
 struct GradLaunch {
   static void go(hipStream_t st, const GradArgs& a, int scoring) {
-    const dim3 grid(token_blocks(a.T));
+    constexpr int kTokens = kWavesPerBlock * kWave / LT;
+    const dim3 grid((a.T + kTokens - 1) / kTokens);
+    const size_t lds = a.d_weights ? size_t(kTokens) * a.E * 4 : 0;
     if (scoring == MOE_SCORE_SIGMOID)
-      route_gradient<Tz, V, true><<<grid, kBlock, 0, st>>>(a);
+      route_gradient<Tz, LT, V, true><<<grid, kBlock, lds, st>>>(a);
     else
-      route_gradient<Tz, V, false><<<grid, kBlock, 0, st>>>(a);
+      route_gradient<Tz, LT, V, false><<<grid, kBlock, lds, st>>>(a);
   }
 };
 
-template <typename Tz, int V>
+template <typename Tz, int LT, int V>
 struct BalanceLaunch {
   static void go(hipStream_t st, const BalanceArgs& a, int scoring, int tiles) {
-    const size_t lds = (size_t(a.E) * (kTileWaves / 2 + 1) + 1) * 4;
+    const size_t lds = (size_t(a.E) * (kTileWaves + 1) + 1) * 4;
     if (scoring == MOE_SCORE_SIGMOID)
-      balance_tiles<Tz, V, true><<<tiles, kTileThreads, lds, st>>>(a);
+      balance_tiles<Tz, LT, V, true><<<tiles, kTileThreads, lds, st>>>(a);
     else
-      balance_tiles<Tz, V, false><<<tiles, kTileThreads, lds, st>>>(a);
+      balance_tiles<Tz, LT, V, false><<<tiles, kTileThreads, lds, st>>>(a);
   }
 };
 
-// Tiles of the balance loss: at most 128 of them, of 32 tokens or more.
-constexpr int kMaxTiles = 128;
+// Calls F<Tz, LT, V>::go for the lanes per token and registers that E takes.
+template <template <typename, int, int> class F, typename Tz, typename... Args>
+void by_tokens(int E, Args&&... args) {
+  const int v = (E + 15) / 16;
+  if (v <= 4) return F<Tz, 16, 4>::go(args...);
+  if (v <= 8) return F<Tz, 16, 8>::go(args...);
+  if (v <= 16) return F<Tz, 16, 16>::go(args...);
+  if (v <= 24) return F<Tz, 16, 24>::go(args...);
+  if (v <= 32) return F<Tz, 16, 32>::go(args...);
+  return F<Tz, 64, 16>::go(args...);
+}
+
+template <template <typename, int, int> class F, typename... Args>
+void by_type_tokens(int type, int E, Args&&... args) {
+  if (type == MOE_TYPE_F32) return by_tokens<F, float>(E, args...);
+  if (type == MOE_TYPE_BF16) return by_tokens<F, __bf16>(E, args...);
+  return by_tokens<F, _Float16>(E, args...);
+}
+
+// Tiles of the balance loss: at most 256, of a multiple of 32 tokens (a
+// workgroup's pass). Measured at T = 16384: XX
+constexpr int kMaxTiles = 256;
+constexpr int kPass = kTileWaves * 4;
 int balance_tile(int T) {
   const int least = (T + kMaxTiles - 1) / kMaxTiles;
-  return std::max(32, (least + kTileWaves - 1) / kTileWaves * kTileWaves);
+  return std::max(1, (least + kPass - 1) / kPass) * kPass;
 }
 int balance_tile_count(int T) {
   const int tile = balance_tile(T);
   return (T + tile - 1) / tile;
+}
+
+// The workspace: terms [S * columns] doubles, sums and pairs [slots * E], used
+// [slots], done [S].
+struct BalanceSpace {
+  size_t terms, slots, bytes;
+  int columns;
+};
+BalanceSpace balance_space(const moe_shape_t& sh, int sequences) {
+  BalanceSpace b;
+  b.columns = (sh.E + kColumn - 1) / kColumn;
+  b.terms = size_t(sequences) * b.columns;
+  b.slots = size_t(balance_tile_count(sh.T)) + sequences;
+  b.bytes = b.terms * 8 + b.slots * (size_t(sh.E) * 8 + 4) + size_t(sequences) * 4;
+  return b;
 }
 
 }  // namespace
@@ -622,8 +1143,17 @@ int moe_route(const moe_shape_t* shape, const moe_router_t* router, int logits_t
   const RouteArgs a{logits, bias, token_mask, topk_ids, topk_weights, err_word, shape->T,
                     shape->E, shape->k, router->renorm, router->scale, router->groups,
                     router->top_groups};
-  by_type<RouteLaunch>(logits_type, shape->E, static_cast<hipStream_t>(stream), a,
-                       router->scoring);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const bool rows = shape->E <= 512 &&
+                    (a.groups == 1 || (a.groups <= 16 && shape->E / a.groups % 16 == 0));
+  if (!rows)
+    by_type<RouteWideLaunch>(logits_type, shape->E, st, a, router->scoring);
+  else if (logits_type == MOE_TYPE_F32)
+    RouteLaunch<float>::go(st, a, router->scoring);
+  else if (logits_type == MOE_TYPE_BF16)
+    RouteLaunch<__bf16>::go(st, a, router->scoring);
+  else
+    RouteLaunch<_Float16>::go(st, a, router->scoring);
   return launch_status();
 }
 
@@ -649,15 +1179,14 @@ int moe_route_backward(const moe_shape_t* shape, const moe_router_t* router, int
   const GradArgs a{logits, topk_ids, d_weights, d_loss, expert_counts, token_counts, seq_offsets,
                    d_logits, err_word, shape->T, shape->E, shape->k, sequences, router->renorm,
                    router->scale};
-  by_type<GradLaunch>(logits_type, shape->E, static_cast<hipStream_t>(stream), a,
-                      router->scoring);
+  by_type_tokens<GradLaunch>(logits_type, shape->E, static_cast<hipStream_t>(stream), a,
+                             router->scoring);
   return launch_status();
 }
 
 size_t moe_balance_workspace_bytes(const moe_shape_t* shape, int sequences) {
   if (!shape_ok(shape) || sequences < 1 || sequences > kMaxSequences) return 0;
-  const size_t slots = size_t(balance_tile_count(shape->T)) + sequences;
-  return slots * (size_t(shape->E) * 8 + 4);
+  return balance_space(*shape, sequences).bytes;
 }
 
 int moe_balance_loss(const moe_shape_t* shape, const moe_router_t* router, int logits_type,
@@ -675,16 +1204,20 @@ int moe_balance_loss(const moe_shape_t* shape, const moe_router_t* router, int l
       !aligned(seq_offsets, 4) || !aligned(loss, 4) || !aligned(expert_counts, 4) ||
       !aligned(token_counts, 4) || !aligned(score_mean, 4) || !aligned(workspace, 16))
     return MOE_ERR_ARG;
-  const int tiles = balance_tile_count(shape->T);
-  const size_t slots = size_t(tiles) + sequences;
-  float* sums = static_cast<float*>(workspace);
-  int32_t* pairs = reinterpret_cast<int32_t*>(sums + slots * shape->E);
-  const BalanceArgs a{logits, topk_ids, seq_offsets, sums, pairs, pairs + slots * shape->E, loss,
-                      expert_counts, token_counts, score_mean, err_word, shape->T, shape->E,
-                      shape->k, sequences, balance_tile(shape->T)};
+  const BalanceSpace space = balance_space(*shape, sequences);
+  double* terms = static_cast<double*>(workspace);
+  float* sums = reinterpret_cast<float*>(terms + space.terms);
+  int32_t* pairs = reinterpret_cast<int32_t*>(sums + space.slots * shape->E);
+  int32_t* used = pairs + space.slots * shape->E;
+  const BalanceArgs a{logits, topk_ids, seq_offsets, sums, pairs, used, terms,
+                      reinterpret_cast<uint32_t*>(used + space.slots), loss, expert_counts,
+                      token_counts, score_mean, err_word, shape->T, shape->E, shape->k, sequences,
+                      balance_tile(shape->T)};
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (tiles > 0) by_type<BalanceLaunch>(logits_type, shape->E, st, a, router->scoring, tiles);
-  balance_join<<<sequences, kTileThreads, 0, st>>>(a);
+  // with T = 0 too: the first kernel clears what the second counts in
+  by_type_tokens<BalanceLaunch>(logits_type, shape->E, st, a, router->scoring,
+                                std::max(1, balance_tile_count(shape->T)));
+  balance_join<<<sequences * space.columns, 1024, 0, st>>>(a);
   return launch_status();
 }
 
