@@ -14,9 +14,8 @@
 //                  from the balance loss's
 //  balance_tiles   one workgroup per tile of tokens: the sums of the scores
 //                  and the pairs of each expert, sequence by sequence
-//  balance_join    one workgroup per (sequence, 64 experts): joins the tiles'
-//                  sums, the loss ([EP]: the busiest GPU's experts set the time
-//                  of a layer)
+//  balance_join    one workgroup per sequence: joins the tiles' sums, the loss
+//                  ([EP]: the busiest GPU's experts set the time of a layer)
 // All of them read the logits once. No result depends on the order in which
 // waves run.
 
@@ -583,44 +582,38 @@ __device__ __forceinline__ bool token_any(bool p) {
   return LT == 16 ? row_any(p) : __ballot(p) != 0;
 }
 
-// e^x for x <= 88 to about 1.5 roundings: 2^(x log2 e) with the product's
-// rounding put right; below e^-104 it is 0.
-__device__ __forceinline__ float exp_near(float x) {
-  constexpr float kLog2e = 1.44269504089f, kLn2 = 0.693147180560f;
-  x = __builtin_amdgcn_fmed3f(x, -104.0f, 88.0f);
-  const float h = x * kLog2e;
-  const float rest = fmaf(x, kLog2e, -h) + x * 1.925963033e-8f;  // log2 e beyond its float
-  const float r = __builtin_amdgcn_exp2f(h);
-  return fmaf(r, rest * kLn2, r);
-}
-
 // A token's scores scaled to a sum of one (p), and for sigmoid 1 - s of each
 // (inner). Masked experts, and those past E, have -infinity and get 0.
+// e^x is 2^(x log2 e) with the product in 32 bits: off by |x| 2^-24 and the
+// instruction's own rounding, which is least where the shares are large (the
+// gradient at T = 16384, E = 256 is 9e-8 off the 64-bit formula, 1e-7 with a
+// full-length exponential, which takes five steps more per expert).
 template <int LT, int V, bool kSigmoid>
 __device__ __forceinline__ void shares(const float (&z)[V], float (&p)[V], float (&inner)[V]) {
+  constexpr float kLog2e = 1.44269504089f;
   float m = z[0];
 #pragma unroll
   for (int i = 1; i < V; ++i) m = fmaxf(m, z[i]);
   m = token_max<LT>(m);
   if (m == -INFINITY) m = 0.0f;  // no expert has a score: all shares are 0
+  const float top = -m * kLog2e;
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     if (kSigmoid) {
-      const float en = exp_near(-z[i]);
+      const float en = __builtin_amdgcn_exp2f(z[i] * -kLog2e);
       p[i] = __builtin_amdgcn_rcpf(1.0f + en);
-      inner[i] = en * p[i];
+      inner[i] = fminf(en, 1e38f) * p[i];
     } else {
-      p[i] = exp_near(z[i] - m);
+      p[i] = __builtin_amdgcn_exp2f(fmaf(z[i], kLog2e, top));
     }
-    p[i] = z[i] == -INFINITY ? 0.0f : p[i];
   }
   if (kSigmoid && __ballot(m < -40.0f)) {
     // all sigmoids of some token are tiny: there they are taken times e^-m
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (m < -40.0f) {
-        p[i] = z[i] == -INFINITY ? 0.0f : exp_near(z[i] - m);  // 1 + e^z is 1
+        p[i] = __builtin_amdgcn_exp2f(fmaf(z[i], kLog2e, top));  // 1 + e^z is 1
         inner[i] = 1.0f;
       }
   }
@@ -632,62 +625,71 @@ __device__ __forceinline__ void shares(const float (&z)[V], float (&p)[V], float
   for (int i = 0; i < V; ++i) p[i] *= inv;
 }
 
-// The logits of a token with E experts; -infinity where it takes no part.
-template <typename Tz, int LT, int V>
-__device__ __forceinline__ void token_logits(const Tz* row, int l, int E, bool used,
-                                             float (&z)[V]) {
-  Tz raw[V];
+// The logits of a token with E experts, all loads at once (kFull: E is V * LT;
+// else of clamped places); as floats, -infinity past E or where the token takes
+// no part.
+template <typename Tz, int LT, int V, bool kFull>
+__device__ __forceinline__ void load_token(const Tz* row, int l, int E, Tz (&raw)[V]) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) raw[i] = row[min(i * LT + l, E - 1)];  // all at once
+  for (int i = 0; i < V; ++i) raw[i] = row[kFull ? i * LT + l : min(i * LT + l, E - 1)];
+}
+template <typename Tz, int LT, int V, bool kFull>
+__device__ __forceinline__ void to_floats(const Tz (&raw)[V], int l, int E, bool used,
+                                          float (&z)[V]) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) z[i] = used && i * LT + l < E ? float(raw[i]) : -INFINITY;
+  for (int i = 0; i < V; ++i)
+    z[i] = used && (kFull || i * LT + l < E) ? float(raw[i]) : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
 // Balance loss
 
-// The sequence of token t: the first s with offsets[s + 1] > t (S when none),
-// by bisection; whatever the offsets hold, the answer is in [0, S].
+// The sequence of the token t that LT lanes share: the first s with
+// offsets[s + 1] > t (S when none). The lanes look at LT places at a time, so
+// that up to LT sequences take one load's time; whatever the offsets hold, the
+// answer is in [0, S].
+template <int LT>
 __device__ __forceinline__ int sequence_of(const int32_t* offsets, int S, int64_t t) {
-  int lo = 0, hi = S;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (offsets[mid + 1] > t)
-      hi = mid;
-    else
-      lo = mid + 1;
+  const int lane = lane_id(), l = lane % LT;
+  int lo = 0;
+  for (int n = S; n > 0;) {  // it is one of lo .. lo + n
+    const int step = (n + LT - 1) / LT;
+    const int behind = (l + 1) * step - 1;
+    const bool below = behind < n && lo + behind < S && offsets[lo + behind + 1] <= t;
+    const uint64_t b = __ballot(below) >> (LT == 16 ? lane & 48 : 0);
+    lo += (LT == 16 ? __popc(uint32_t(b) & 0xFFFF) : __popcll(b)) * step;
+    n = step - 1;
   }
-  return lo;
+  return min(lo, S);
 }
 
 struct BalanceArgs {
   const void* logits;
   const int32_t* ids;
   const int32_t* offsets;  // NULL: one sequence of all tokens
-  float* sums;             // [slots * E] sums of the scores, slots = tiles + S
-  int32_t* pairs;          // [slots * E] pairs
+  float* sums;             // [slots * stride] sums of the scores, slots = tiles + S
+  int32_t* pairs;          // [slots * stride] pairs
   int32_t* used;           // [slots] tokens with an expert
-  double* terms;           // [S * columns] parts of the loss
-  uint32_t* done;          // [S] columns that are joined
   float* loss;
   int32_t* counts;
   int32_t* tokens;
   float* mean;
   int32_t* err;
   int T, E, k, S, tile;
+  int stride;              // E rounded up to a multiple of 4
 };
 
 constexpr int kTileThreads = 512;
 constexpr int kTileWaves = kTileThreads / kWave;
-constexpr int kColumn = 64;  // experts that a workgroup joins
 
-// One workgroup per tile of tokens, each wave 64 / LT tokens at a time; the
-// scores are summed per lane in registers. Where a sequence ends within the
-// tile, the sums so far go to the slot tile + sequence (increasing along the
-// tokens, so no two pairs of them share one) and start anew. Bound by
-// latency: T = 16384, E = 256 with sigmoids of bfloat16 logits (8.4 MB) takes
-// XX us; with a wave per token it was 23.7 us.
-template <typename Tz, int LT, int V, bool kSigmoid>
+// One workgroup per tile of tokens, each wave 64 / LT tokens at a time (the
+// next ones' logits on their way); the scores are summed per lane in
+// registers. Where a sequence ends within the tile, the sums so far go to the
+// slot tile + sequence (increasing along the tokens, so no two pairs of them
+// share one) and start anew. Bound by latency: T = 16384, E = 256 with
+// sigmoids of bfloat16 logits (8.4 MB) takes 9.6 us (23.7 us with a wave per
+// token), T = 4096, E = 384 in float32 5.8 us.
+template <typename Tz, int LT, int V, bool kSigmoid, bool kFull>
 __global__ __launch_bounds__(kTileThreads) void balance_tiles(BalanceArgs a) {
   extern __shared__ float lds_all[];
   const int E = a.E;
@@ -695,36 +697,39 @@ __global__ __launch_bounds__(kTileThreads) void balance_tiles(BalanceArgs a) {
   int* used = pairs + E;                         // [1]
   float* part = lds_all + E + 1;                 // [waves * E]
   constexpr int kTokens = kWave / LT;
+  constexpr int kPass = kTileWaves * kTokens;
   const int wave = wave_in_block(), lane = lane_id(), l = lane % LT;
   const int64_t begin = (int64_t)blockIdx.x * a.tile;
   const int64_t end = min(begin + a.tile, (int64_t)a.T);
-  // the joining workgroups' counts start at 0 (this kernel runs before them)
-  for (int64_t i = (int64_t)blockIdx.x * kTileThreads + threadIdx.x; i < a.S;
-       i += (int64_t)gridDim.x * kTileThreads)
-    a.done[i] = 0;
-  int s = a.offsets ? sequence_of(a.offsets, a.S, begin) : 0;
+  int s = a.offsets ? sequence_of<kWave>(a.offsets, a.S, begin) : 0;
   for (; s < a.S; ++s) {
     const int64_t first = a.offsets ? max((int64_t)a.offsets[s], begin) : begin;
     const int64_t last = a.offsets ? min((int64_t)a.offsets[s + 1], end) : end;
     if (first >= end) break;
     if (first >= last) continue;
+    const int64_t mine = first + wave * kTokens + lane / LT;
+    Tz raw[V];
+    int id = -1;
+    auto load = [&](int64_t t) {  // past the last token: the last one's, not used
+      const int64_t at = min(t, last - 1);
+      load_token<Tz, LT, V, kFull>(static_cast<const Tz*>(a.logits) + at * E, l, E, raw);
+      id = t < last && l < a.k ? a.ids[at * a.k + l] : -1;
+    };
+    load(mine);
     for (int e = threadIdx.x; e <= E; e += kTileThreads) pairs[e] = 0;
     __syncthreads();
     float sum[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) sum[i] = 0.0f;
-    for (int64_t t0 = first + wave * kTokens; t0 < last; t0 += kTileWaves * kTokens) {
-      const int64_t t = t0 + lane / LT;
-      const bool here = t < last;
-      const int64_t at = min(t, last - 1);
-      const int id = here && l < a.k ? a.ids[at * a.k + l] : -1;
+    for (int64_t t = mine; t - lane / LT < last; t += kPass) {
       float z[V], p[V], inner[V];
       const bool ok = id >= 0 && id < E;
       if (__ballot(id < -1 || id >= E) && lane == 0) flag_error(a.err, MOE_ERRBIT_BAD_ID);
       if (ok) atomicAdd(pairs + id, 1);  // integers: any order gives the same count
       const bool counted = token_any<LT>(ok);
       if (counted && l == 0) atomicAdd(used, 1);
-      token_logits<Tz, LT, V>(static_cast<const Tz*>(a.logits) + at * E, l, E, counted, z);
+      to_floats<Tz, LT, V, kFull>(raw, l, E, counted, z);
+      if (t - lane / LT + kPass < last) load(t + kPass);
       shares<LT, V, kSigmoid>(z, p, inner);
 #pragma unroll
       for (int i = 0; i < V; ++i) sum[i] += p[i];
@@ -736,7 +741,7 @@ __global__ __launch_bounds__(kTileThreads) void balance_tiles(BalanceArgs a) {
         sum[i] += __shfl_xor(sum[i], 16);
         sum[i] += __shfl_xor(sum[i], 32);
       }
-      if (lane < LT && i * LT + l < E) part[wave * E + i * LT + l] = sum[i];
+      if (lane < LT && (kFull || i * LT + l < E)) part[wave * E + i * LT + l] = sum[i];
     }
     __syncthreads();
     const int64_t slot = (int64_t)blockIdx.x + s;
@@ -744,25 +749,30 @@ __global__ __launch_bounds__(kTileThreads) void balance_tiles(BalanceArgs a) {
       float total = 0.0f;
 #pragma unroll
       for (int w = 0; w < kTileWaves; ++w) total += part[w * E + e];
-      a.sums[slot * E + e] = total;
-      a.pairs[slot * E + e] = pairs[e];
+      a.sums[slot * a.stride + e] = total;
+      a.pairs[slot * a.stride + e] = pairs[e];
     }
     if (threadIdx.x == 0) a.used[slot] = *used;
     __syncthreads();
   }
 }
 
-// One workgroup per (sequence, 64 experts). The tiles' sums of an expert are
-// added by 16 threads, in an order that the sizes alone fix, in 64 bits. The
-// workgroup that finishes a sequence last adds up the loss's parts, in order.
-__global__ __launch_bounds__(1024) void balance_join(BalanceArgs a) {
-  constexpr int kSlices = 1024 / kColumn;
-  __shared__ double lds_sum[1024];
-  __shared__ int lds_pairs[1024];
+// One workgroup per sequence: a thread adds up four experts' sums of every
+// slices-th tile, then the slices are joined, all in an order that the sizes
+// alone fix and in 64 bits. (A workgroup per 64 experts, the last of them
+// adding up the loss, took 7.3 us for 13 sequences of 16384 tokens where this
+// takes 5.7, and 7.5 against 7.8 us for one of 4096: the fence and the count
+// between workgroups cost what reading from more of them gave.)
+constexpr int kJoinThreads = 1024;
+constexpr int kJoinSlices = 32;  // at most
+__global__ __launch_bounds__(kJoinThreads) void balance_join(BalanceArgs a) {
+  typedef float float4v __attribute__((ext_vector_type(4)));
+  typedef int int4v __attribute__((ext_vector_type(4)));
+  __shared__ double lds_sum[kJoinThreads * 4];
+  __shared__ int lds_pairs[kJoinThreads * 4];
+  __shared__ double lds_term[kJoinThreads / kWave];
   __shared__ int lds_used;
-  __shared__ bool lds_last;
-  const int E = a.E, columns = (E + kColumn - 1) / kColumn;
-  const int s = blockIdx.x / columns, column = blockIdx.x % columns, tid = threadIdx.x;
+  const int E = a.E, s = blockIdx.x, tid = threadIdx.x;
   int64_t first = a.offsets ? a.offsets[s] : 0, last = a.offsets ? a.offsets[s + 1] : a.T;
   if (first < 0 || last > a.T || first > last) {
     if (tid == 0) flag_error(a.err, MOE_ERRBIT_BAD_SEQ);
@@ -773,48 +783,62 @@ __global__ __launch_bounds__(1024) void balance_join(BalanceArgs a) {
   if (tid == 0) lds_used = 0;
   __syncthreads();
   int n = 0;
-  for (int64_t w = w0 + tid; w < w1; w += 1024) n += a.used[w + s];
+  for (int64_t w = w0 + tid; w < w1; w += kJoinThreads) n += a.used[w + s];
   if (n) atomicAdd(&lds_used, n);
-  const int e = column * kColumn + tid % kColumn, slice = tid / kColumn;
-  double sum = 0.0;
-  int pairs = 0;
-  if (e < E) {
-#pragma unroll 4
-    for (int64_t w = w0 + slice; w < w1; w += kSlices) {
-      sum += a.sums[(w + s) * E + e];
-      pairs += a.pairs[(w + s) * E + e];
+  const int quads = a.stride / 4;  // at most 256
+  const int slices = min(kJoinSlices, kJoinThreads / quads);
+  const int quad = tid % quads, slice = tid / quads;
+  double sum[4] = {0, 0, 0, 0};
+  int pairs[4] = {0, 0, 0, 0};
+  if (slice < slices) {
+    constexpr int kAtOnce = 8;  // loads of either kind on their way
+    for (int64_t w = w0 + slice; w < w1; w += slices * kAtOnce) {
+      float4v x[kAtOnce];
+      int4v c[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int64_t at = (min(w + i * slices, w1 - 1) + s) * a.stride + quad * 4;
+        x[i] = *reinterpret_cast<const float4v*>(a.sums + at);
+        c[i] = *reinterpret_cast<const int4v*>(a.pairs + at);
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        if (w + i * slices < w1)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            sum[q] += x[i][q];
+            pairs[q] += c[i][q];
+          }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      lds_sum[slice * a.stride + quad * 4 + q] = sum[q];
+      lds_pairs[slice * a.stride + quad * 4 + q] = pairs[q];
     }
   }
-  lds_sum[tid] = sum;
-  lds_pairs[tid] = pairs;
   __syncthreads();
   n = lds_used;
-  if (tid < kColumn) {
-    for (int q = 1; q < kSlices; ++q) {
-      sum += lds_sum[q * kColumn + tid];
-      pairs += lds_pairs[q * kColumn + tid];
+  double term = 0.0;
+  if (tid < E) {
+    double total = 0.0;
+    int count = 0;
+    for (int q = 0; q < slices; ++q) {
+      total += lds_sum[q * a.stride + tid];
+      count += lds_pairs[q * a.stride + tid];
     }
-    const double mean = n > 0 ? sum / n : 0.0;
-    if (e < E) {
-      a.counts[(int64_t)s * E + e] = pairs;
-      a.mean[(int64_t)s * E + e] = float(mean);
-    }
-    double term = mean * pairs;  // the wave's 64 experts, by halves
-    for (int h = kColumn / 2; h > 0; h >>= 1) term += __shfl_xor(term, h);
-    if (tid == 0) {
-      a.terms[(int64_t)s * columns + column] = term;
-      __threadfence();
-      lds_last = atomicAdd(a.done + s, 1u) + 1 == uint32_t(columns);
-      if (lds_last) {
-        __threadfence();
-        double total = 0.0;
-        for (int c = 0; c < columns; ++c)
-          total += __hip_atomic_load(a.terms + (int64_t)s * columns + c, __ATOMIC_RELAXED,
-                                     __HIP_MEMORY_SCOPE_AGENT);
-        a.tokens[s] = n;
-        a.loss[s] = n > 0 ? float(total * E / (double(a.k) * n)) : 0.0f;
-      }
-    }
+    const double mean = n > 0 ? total / n : 0.0;
+    a.counts[(int64_t)s * E + tid] = count;
+    a.mean[(int64_t)s * E + tid] = float(mean);
+    term = mean * count;
+  }
+  for (int h = kWave / 2; h > 0; h >>= 1) term += __shfl_xor(term, h);
+  if (lane_id() == 0) lds_term[wave_in_block()] = term;
+  __syncthreads();
+  if (tid == 0) {
+    double total = 0.0;
+    for (int w = 0; w < kJoinThreads / kWave; ++w) total += lds_term[w];
+    a.tokens[s] = n;
+    a.loss[s] = n > 0 ? float(total * E / (double(a.k) * n)) : 0.0f;
   }
 }
 
@@ -845,9 +869,9 @@ struct GradArgs {
 // changes nothing in u_e - sum p u, so k T' / E is taken off n_e first: what
 // is left to cancel is the imbalance, not the counts.
 // The slots' parts reach their experts' lanes through LDS. Bound by the bytes:
-// T = 16384, E = 256 in float32 (33.6 MB both ways) takes XX us, 13.8 us
-// with a wave per token.
-template <typename Tz, int LT, int V, bool kSigmoid>
+// T = 16384, E = 256 in float32 (33.6 MB both ways) takes 9.9 us, 13.8 us
+// with a wave per token; T = 8192 in bfloat16 with both gradients 6.2 us.
+template <typename Tz, int LT, int V, bool kSigmoid, bool kFull>
 __global__ __launch_bounds__(kBlock) void route_gradient(GradArgs a) {
   constexpr int kTokens = kWave / LT;
   extern __shared__ float lds_all[];
@@ -860,6 +884,8 @@ __global__ __launch_bounds__(kBlock) void route_gradient(GradArgs a) {
   const bool here = t < a.T;
   const int64_t at = min(t, (int64_t)a.T - 1);
   const Tz* row = static_cast<const Tz*>(a.logits) + at * E;
+  Tz raw[V];
+  load_token<Tz, LT, V, kFull>(row, l, E, raw);
   const int id = here && l < k ? a.ids[at * k + l] : -1;
   const bool ok = id >= 0 && id < E;
   if (__ballot(id < -1 || id >= E) && lane == 0) flag_error(a.err, MOE_ERRBIT_BAD_ID);
@@ -867,12 +893,12 @@ __global__ __launch_bounds__(kBlock) void route_gradient(GradArgs a) {
   int s = 0;
   bool inside = used && a.d_loss;
   if (a.d_loss && a.offsets) {
-    s = sequence_of(a.offsets, a.S, at);
+    s = sequence_of<LT>(a.offsets, a.S, at);
     inside = inside && s < a.S && a.offsets[min(s, a.S - 1)] <= t;
     s = min(s, a.S - 1);
   }
   float z[V], d[V], u[V];
-  token_logits<Tz, LT, V>(row, l, E, used, z);
+  to_floats<Tz, LT, V, kFull>(raw, l, E, used, z);
 #pragma unroll
   for (int i = 0; i < V; ++i) d[i] = u[i] = 0.0f;
   const bool dense = !kSigmoid && !a.renorm && a.d_weights;
@@ -902,7 +928,7 @@ __global__ __launch_bounds__(kBlock) void route_gradient(GradArgs a) {
     // expert's place shares it: then the slots add one after the other.
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (i * LT + l < E) spread[i * LT + l] = 0.0f;
+      if (kFull || i * LT + l < E) spread[i * LT + l] = 0.0f;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     if (ok) spread[id] = float(l);
@@ -926,7 +952,7 @@ __global__ __launch_bounds__(kBlock) void route_gradient(GradArgs a) {
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float v = i * LT + l < E ? spread[i * LT + l] : 0.0f;
+      const float v = kFull || i * LT + l < E ? spread[i * LT + l] : 0.0f;
       if (dense)
         u[i] = v;
       else
@@ -939,12 +965,13 @@ __global__ __launch_bounds__(kBlock) void route_gradient(GradArgs a) {
     const float rate = inside && n > 0 ? float(double(a.d_loss[s]) * E /
                                                (double(k) * double(n) * double(n)))
                                        : 0.0f;
-    const float off = float(double(k) * n / E);
+    const float off = -rate * float(double(k) * n / E);
     int count[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) count[i] = a.counts[(int64_t)s * E + min(i * LT + l, E - 1)];
+    for (int i = 0; i < V; ++i)
+      count[i] = a.counts[(int64_t)s * E + (kFull ? i * LT + l : min(i * LT + l, E - 1))];
 #pragma unroll
-    for (int i = 0; i < V; ++i) u[i] += rate * (float(count[i]) - off);
+    for (int i = 0; i < V; ++i) u[i] += fmaf(rate, float(count[i]), off);
   }
   if (dense || a.d_loss) {
     float p[V], inner[V];
@@ -955,16 +982,15 @@ __global__ __launch_bounds__(kBlock) void route_gradient(GradArgs a) {
     dot = token_sum<LT>(dot);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      float v = p[i] * (u[i] - dot);
-      if (kSigmoid) v *= inner[i];
-      d[i] += used && p[i] != 0.0f ? v : 0.0f;
+      const float v = kSigmoid ? p[i] * inner[i] : p[i];
+      d[i] = fmaf(v, u[i] - dot, d[i]);
     }
   }
   if (!here) return;
   Tz* out = static_cast<Tz*>(a.d_logits) + t * E;
 #pragma unroll
   for (int i = 0; i < V; ++i)
-    if (i * LT + l < E) out[i * LT + l] = Tz(d[i]);
+    if (kFull || i * LT + l < E) out[i * LT + l] = Tz(d[i]);
 }
 
 // ---------------------------------------------------------------------------
@@ -1061,10 +1087,12 @@ struct GradLaunch {
     constexpr int kTokens = kWavesPerBlock * kWave / LT;
     const dim3 grid((a.T + kTokens - 1) / kTokens);
     const size_t lds = a.d_weights ? size_t(kTokens) * a.E * 4 : 0;
-    if (scoring == MOE_SCORE_SIGMOID)
-      route_gradient<Tz, LT, V, true><<<grid, kBlock, lds, st>>>(a);
-    else
-      route_gradient<Tz, LT, V, false><<<grid, kBlock, lds, st>>>(a);
+    const bool full = a.E == V * LT;
+    auto go = full ? scoring == MOE_SCORE_SIGMOID ? route_gradient<Tz, LT, V, true, true>
+                                                  : route_gradient<Tz, LT, V, false, true>
+                   : scoring == MOE_SCORE_SIGMOID ? route_gradient<Tz, LT, V, true, false>
+                                                  : route_gradient<Tz, LT, V, false, false>;
+    go<<<grid, kBlock, lds, st>>>(a);
   }
 };
 
@@ -1072,10 +1100,12 @@ template <typename Tz, int LT, int V>
 struct BalanceLaunch {
   static void go(hipStream_t st, const BalanceArgs& a, int scoring, int tiles) {
     const size_t lds = (size_t(a.E) * (kTileWaves + 1) + 1) * 4;
-    if (scoring == MOE_SCORE_SIGMOID)
-      balance_tiles<Tz, LT, V, true><<<tiles, kTileThreads, lds, st>>>(a);
-    else
-      balance_tiles<Tz, LT, V, false><<<tiles, kTileThreads, lds, st>>>(a);
+    const bool full = a.E == V * LT;
+    auto go = full ? scoring == MOE_SCORE_SIGMOID ? balance_tiles<Tz, LT, V, true, true>
+                                                  : balance_tiles<Tz, LT, V, false, true>
+                   : scoring == MOE_SCORE_SIGMOID ? balance_tiles<Tz, LT, V, true, false>
+                                                  : balance_tiles<Tz, LT, V, false, false>;
+    go<<<tiles, kTileThreads, lds, st>>>(a);
   }
 };
 
@@ -1099,7 +1129,7 @@ void by_type_tokens(int type, int E, Args&&... args) {
 }
 
 // Tiles of the balance loss: at most 256, of a multiple of 32 tokens (a
-// workgroup's pass). Measured at T = 16384: XX
+// workgroup's pass).
 constexpr int kMaxTiles = 256;
 constexpr int kPass = kTileWaves * 4;
 int balance_tile(int T) {
@@ -1111,20 +1141,11 @@ int balance_tile_count(int T) {
   return (T + tile - 1) / tile;
 }
 
-// The workspace: terms [S * columns] doubles, sums and pairs [slots * E], used
-// [slots], done [S].
-struct BalanceSpace {
-  size_t terms, slots, bytes;
-  int columns;
-};
-BalanceSpace balance_space(const moe_shape_t& sh, int sequences) {
-  BalanceSpace b;
-  b.columns = (sh.E + kColumn - 1) / kColumn;
-  b.terms = size_t(sequences) * b.columns;
-  b.slots = size_t(balance_tile_count(sh.T)) + sequences;
-  b.bytes = b.terms * 8 + b.slots * (size_t(sh.E) * 8 + 4) + size_t(sequences) * 4;
-  return b;
+// The workspace: sums and pairs [slots * stride], used [slots].
+size_t balance_slots(const moe_shape_t& sh, int sequences) {
+  return size_t(balance_tile_count(sh.T)) + sequences;
 }
+int balance_stride(const moe_shape_t& sh) { return (sh.E + 3) / 4 * 4; }
 
 }  // namespace
 
@@ -1186,7 +1207,7 @@ int moe_route_backward(const moe_shape_t* shape, const moe_router_t* router, int
 
 size_t moe_balance_workspace_bytes(const moe_shape_t* shape, int sequences) {
   if (!shape_ok(shape) || sequences < 1 || sequences > kMaxSequences) return 0;
-  return balance_space(*shape, sequences).bytes;
+  return balance_slots(*shape, sequences) * (size_t(balance_stride(*shape)) * 8 + 4);
 }
 
 int moe_balance_loss(const moe_shape_t* shape, const moe_router_t* router, int logits_type,
@@ -1204,20 +1225,16 @@ int moe_balance_loss(const moe_shape_t* shape, const moe_router_t* router, int l
       !aligned(seq_offsets, 4) || !aligned(loss, 4) || !aligned(expert_counts, 4) ||
       !aligned(token_counts, 4) || !aligned(score_mean, 4) || !aligned(workspace, 16))
     return MOE_ERR_ARG;
-  const BalanceSpace space = balance_space(*shape, sequences);
-  double* terms = static_cast<double*>(workspace);
-  float* sums = reinterpret_cast<float*>(terms + space.terms);
-  int32_t* pairs = reinterpret_cast<int32_t*>(sums + space.slots * shape->E);
-  int32_t* used = pairs + space.slots * shape->E;
-  const BalanceArgs a{logits, topk_ids, seq_offsets, sums, pairs, used, terms,
-                      reinterpret_cast<uint32_t*>(used + space.slots), loss, expert_counts,
-                      token_counts, score_mean, err_word, shape->T, shape->E, shape->k, sequences,
-                      balance_tile(shape->T)};
+  const int tiles = balance_tile_count(shape->T), stride = balance_stride(*shape);
+  const size_t slots = balance_slots(*shape, sequences);
+  float* sums = static_cast<float*>(workspace);
+  int32_t* pairs = reinterpret_cast<int32_t*>(sums + slots * stride);
+  const BalanceArgs a{logits, topk_ids, seq_offsets, sums, pairs, pairs + slots * stride, loss,
+                      expert_counts, token_counts, score_mean, err_word, shape->T, shape->E,
+                      shape->k, sequences, balance_tile(shape->T), stride};
   hipStream_t st = static_cast<hipStream_t>(stream);
-  // with T = 0 too: the first kernel clears what the second counts in
-  by_type_tokens<BalanceLaunch>(logits_type, shape->E, st, a, router->scoring,
-                                std::max(1, balance_tile_count(shape->T)));
-  balance_join<<<sequences * space.columns, 1024, 0, st>>>(a);
+  if (tiles > 0) by_type_tokens<BalanceLaunch>(logits_type, shape->E, st, a, router->scoring, tiles);
+  balance_join<<<sequences, kJoinThreads, 0, st>>>(a);
   return launch_status();
 }
 
