@@ -740,6 +740,8 @@ def balance_loss(logits: torch.Tensor, topk_ids, router: Router, loss, expert_co
     T, E = logits.shape
     if topk_ids.dim() != 2:
         raise MoeError(f"topk_ids has shape {tuple(topk_ids.shape)}, the call needs [T, k]")
+    if workspace is None:
+        raise MoeError("balance_loss needs a workspace of balance_workspace_bytes bytes")
     k, S = topk_ids.shape[1], loss.numel()
     i32, f32 = torch.int32, torch.float32
     _call(lib().moe_balance_loss, "moe_balance_loss", dev, _sizes(T, 8, E, k),

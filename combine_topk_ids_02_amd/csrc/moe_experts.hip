@@ -43,6 +43,7 @@ constexpr int kTile = 16;    // an MFMA tile: 16 weight rows, 16 buffer rows
 constexpr int NT = 2;        // tiles of weight rows per wave
 constexpr int kDepth = 2;    // granules of H that a wave has on their way
 constexpr int kChunk = 32;   // values of H in 16 bytes of codes
+constexpr int kMostGroups = 1 << 22;
 
 struct ProductArgs {
   const uint16_t* rows;
@@ -493,7 +494,9 @@ int moe_expert_product(const moe_shape_t* shape, int N, int format, int act,
   const int64_t active = std::min<int64_t>(shape->E, pairs);
   const int form = form_of(*shape, swiglu, wide, pairs, active);
   const int tiles = column_tiles(form, swiglu, wide);
-  const int64_t most = INT32_MAX / tiles / 2;
+  // A launch has fewer than 2^32 threads: fewer slots than chunks, and a
+  // workgroup takes several, where N is very large.
+  const int64_t most = std::max(1, kMostGroups / 2 / tiles);
   const int firsts = int(std::min(active, most));
   const int beyonds = int(std::min((pairs - 1) / kForms[form].rows, most));
   const ProductArgs a{rows, expert_counts, expert_offsets, w_q, w_scale, factor, out, err_word,

@@ -28,6 +28,7 @@ using namespace moe;
 constexpr int kBlock = 256;
 constexpr int kWavesPerBlock = kBlock / kWave;
 constexpr int kMaxSequences = 1 << 16;
+constexpr int kMaxTokens = 1 << 25;  // a launch has fewer than 2^32 threads, 64 a token
 
 // Expert e = 64 * i + lane lies in register i of lane e % 64; V registers.
 template <typename Tz, int V>
@@ -999,7 +1000,7 @@ __global__ __launch_bounds__(kBlock) void route_gradient(GradArgs a) {
 size_t type_size(int type) { return type == MOE_TYPE_F32 ? 4 : 2; }
 
 bool router_ok(const moe_shape_t* sh, const moe_router_t* r, int type) {
-  if (!shape_ok(sh) || !r) return false;
+  if (!shape_ok(sh) || !r || sh->T > kMaxTokens) return false;
   if (type != MOE_TYPE_F32 && type != MOE_TYPE_BF16 && type != MOE_TYPE_F16) return false;
   if (r->scoring != MOE_SCORE_SOFTMAX && r->scoring != MOE_SCORE_SIGMOID) return false;
   if (r->renorm != 0 && r->renorm != 1) return false;

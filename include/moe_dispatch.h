@@ -486,7 +486,8 @@ typedef struct moe_router {
  *   token_mask       [T] in:  bytes; a token with 0 is given no expert and its logits are
  *                             not looked at (padding of a batch); or NULL
  *   topk_ids [T*k], topk_weights [T*k]  out
- * Bias and groups > 1 with softmax scoring are argument errors. One launch.
+ * Bias and groups > 1 with softmax scoring are argument errors, and so are more
+ * than 2^25 tokens (here and in the two calls below). One launch.
  */
 int moe_route(const moe_shape_t* shape, const moe_router_t* router, int logits_type,
               const void* logits, const float* bias, const uint8_t* token_mask,

@@ -1,0 +1,204 @@
+"""The router, its gradient, the balance loss and the expert products at the
+ends of their ranges: choices that hang on the last bit between and inside
+groups, lists of candidates that run out, tensors past 2^31 elements, the
+widest product."""
+import numpy as np
+import pytest
+import torch
+
+import combine_topk_ids_02_amd as moe
+import router_ref as ref
+from router_ref import ULP
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU visible: the GPU tests must run on an MI355X")
+    moe.lib()
+
+
+def say(msg):
+    print(msg, flush=True)
+
+
+def choose(z, k, router, bias=None):
+    """z: float32 array; the ids of moe.route."""
+    z_d = torch.from_numpy(np.ascontiguousarray(z, np.float32)).cuda()
+    ids = torch.full((z.shape[0], k), -7, dtype=torch.int32, device="cuda")
+    w = torch.zeros(z.shape[0], k, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    b = None if bias is None else torch.from_numpy(bias).cuda()
+    moe.route(z_d, k, router, ids, w, bias=b, err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and bool(torch.isfinite(w).all())
+    return ids.cpu().numpy()
+
+
+# (E, groups, top_groups, k)
+GROUPED = [(128, 8, 4, 8), (256, 8, 3, 8), (384, 4, 2, 6), (512, 16, 5, 16), (64, 2, 1, 4),
+           (48, 3, 2, 16), (96, 8, 4, 5), (640, 8, 4, 8)]
+
+
+@pytest.mark.parametrize("case", range(len(GROUPED)))
+@pytest.mark.parametrize("kind", ["all", "pairs", "copies"])
+def test_groups_near_ties(case, kind):
+    """Groups whose scores are equal or a few last bits apart: all of them, two
+    of them, and groups that are copies of each other."""
+    E, groups, top, k = GROUPED[case]
+    say(f"[groups] {GROUPED[case]} {kind}")
+    rng = np.random.default_rng(400 + case)
+    T, per = 150, E // groups
+    if kind == "all":
+        base = rng.normal(size=(T, 1)).astype(np.float32)
+        z = base + rng.integers(-4, 5, size=(T, E)).astype(np.float32) * np.spacing(abs(base))
+    else:
+        z = rng.normal(size=(T, groups, per)).astype(np.float32) * np.float32(2)
+        for t in range(T):
+            for _ in range(1 if kind == "pairs" else groups):
+                a, b = rng.integers(0, groups, size=2)
+                z[t, b] = rng.permutation(z[t, a])
+                if kind == "pairs":
+                    z[t, b] += rng.integers(-1, 2, size=per) * np.spacing(abs(z[t, b]))
+        z = z.reshape(T, E)
+    bias = (rng.integers(-2, 3, size=E) * 2.0 ** -24).astype(np.float32) if case % 2 else None
+    got = choose(z, k, moe.Router("sigmoid", True, 1.0, groups, top), bias)
+    want, _ = ref.choose(z, k, "sigmoid", bias, groups, top)
+    assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("E", [60, 128, 250, 256, 300, 384, 500, 512])
+@pytest.mark.parametrize("k", [1, 7, 8, 9, 16])
+def test_best_experts_in_one_column(E, k):
+    """The best experts are all congruent mod 16 (one lane's), and close."""
+    rng = np.random.default_rng(E * 17 + k)
+    z = rng.normal(size=(64, E)).astype(np.float32)
+    for t in range(64):
+        z[t, t % 16::16] += np.float32(8)
+        if t % 4 == 0:  # equal ones among them, or a last bit apart
+            best = z[t, t % 16::16]
+            z[t, t % 16::16] = best[0] + rng.integers(-2, 3, size=best.size) * np.spacing(best[0])
+    for router, bias in ((moe.Router(), None), (moe.Router("sigmoid"), None),
+                         (moe.Router("sigmoid"), (rng.normal(size=E) * 1e-3).astype(np.float32))):
+        want, _ = ref.choose(z, k, "softmax" if router.scoring == 0 else "sigmoid", bias)
+        assert np.array_equal(choose(z, k, router, bias), want)
+
+
+@pytest.mark.parametrize("T,E", [((1 << 21) + 37, 1024), ((1 << 22) + 5, 512)])
+def test_more_than_2_31_logits(T, E):
+    """The last tokens of a batch past 2^31 elements are as they are alone."""
+    say(f"[large] T={T} E={E}")
+    k, n = 3, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    z = torch.empty(T, E, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    router = moe.Router("softmax", False)
+    ids = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, k, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    moe.route(z, k, router, ids, w, err=err)
+    tail = z[T - n:].clone()
+    ids2, w2 = torch.empty_like(ids[:n]), torch.empty_like(w[:n])
+    moe.route(tail, k, router, ids2, w2, err=err)
+    torch.cuda.synchronize()
+    assert torch.equal(ids[T - n:], ids2) and torch.equal(w[T - n:], w2)
+    say("routed")
+
+    off = torch.tensor([0, T - 50, T], dtype=torch.int32, device="cuda")
+    out = [torch.empty(2, device="cuda"), torch.empty(2, E, dtype=torch.int32, device="cuda"),
+           torch.empty(2, dtype=torch.int32, device="cuda"), torch.empty(2, E, device="cuda")]
+    ws = torch.empty(moe.balance_workspace_bytes(T, E, k, 2), dtype=torch.uint8, device="cuda")
+    moe.balance_loss(z, ids, router, *out, workspace=ws, seq_offsets=off, err=err)
+    torch.cuda.synchronize()
+    zt = tail.double().cpu().numpy()
+    wl, wc, wt, wm = ref.balance(zt, ids2.cpu().numpy(), "softmax", np.array([n - 50, n]))
+    assert np.array_equal(out[1][1].cpu().numpy(), wc[0]) and int(out[2][1]) == wt[0] == 50
+    assert int(out[2][0]) == T - 50 and int(out[1].sum()) == T * k
+    # spreads below 12: counted as in test_router_gpu.py
+    mean = out[3].double().cpu().numpy()
+    assert (abs(mean[1] - wm[0]) <= 120 * ULP * wm[0]).all()
+    assert abs(float(out[0][1]) - wl[0]) <= 120 * ULP * wl[0]
+    # a mean of T - 50 shares that sum to one: each a sum of T / 256 / 32 floats
+    # a lane, then 64-bit ones
+    assert abs(mean[0].sum() - 1) <= (120 + T / 8192) * ULP
+    say("balanced")
+
+    dw = torch.randn(T, k, device="cuda", generator=g)
+    dl = torch.tensor([0.5, -2.0], device="cuda")
+    dz = torch.empty_like(z)
+    moe.route_backward(z, ids, router, dz, d_weights=dw, balance=(dl, out[1], out[2], off),
+                       err=err)
+    off2 = torch.tensor([0, n - 50, n], dtype=torch.int32, device="cuda")
+    dz2 = torch.empty_like(tail)
+    moe.route_backward(tail, ids2, router, dz2, d_weights=dw[T - n:].clone(),
+                       balance=(dl, out[1], out[2], off2), err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    assert torch.equal(dz[T - n:], dz2)
+
+
+def product(rows, counts, off, T, k, q, s, act=None):
+    N = q.shape[1] // 2 if act else q.shape[1]
+    out = torch.full((rows.shape[0], N), -77.0, dtype=torch.bfloat16, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    moe.expert_product("mxfp4", rows, torch.tensor(counts, **i32), torch.tensor(off, **i32), T, k,
+                       q, s, out, act=act, err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    return out
+
+
+@pytest.mark.parametrize("n", [3, 40])
+def test_product_past_2_31(n):
+    """The widest rows, weights past 2^32 bytes, rows past 2^31 elements. Codes
+    times +-1, scales of 1: every sum is a whole number of halves below 2^24
+    of them, so float32 holds it and the output is its nearest bf16."""
+    E, N, H, cap = 640, 16, 1 << 20, 2200
+    first = cap - n
+    say(f"[large] n={n}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    q = torch.randint(0, 256, (E, N, H // 2), dtype=torch.uint8, device="cuda", generator=g)
+    s = torch.full((E, N, H // 32), 127, dtype=torch.uint8, device="cuda")
+    rows = torch.full((cap, H), float("nan"), dtype=torch.bfloat16, device="cuda")
+    for r in [0, *range(first, cap)]:
+        rows[r] = torch.randint(-1, 2, (H,), device="cuda", generator=g)
+    counts, off = [0] * E, [first] * (E + 1)
+    counts[0], counts[-1], off[0], off[-1] = 1, n, 0, cap
+    out = product(rows, counts, off, n + 1, 1, q, s)
+    for e, at in ((0, [0]), (E - 1, list(range(first, cap)))):
+        w = ref.weight_values("mxfp4", q[e].cpu().numpy(), s[e].cpu().numpy())
+        want = torch.from_numpy(rows[at].double().cpu().numpy() @ w.T).to(torch.bfloat16)
+        assert torch.equal(out[at].cpu(), want)
+    assert bool((out[1:first] == -77).all())
+
+
+@pytest.mark.parametrize("T,k", [(4, 1), (4096, 16)])
+@pytest.mark.parametrize("act", [None, "swiglu"])
+def test_widest_product(T, k, act):
+    """2^24 weight rows, and many more rows said to be in use than there are."""
+    N, H, n = 1 << 24, 32, 4
+    say(f"[wide] T={T} k={k} {act}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(7)
+    q = torch.randint(0, 256, (1, N, H // 2), dtype=torch.uint8, device="cuda", generator=g)
+    s = torch.full((1, N, 1), 125, dtype=torch.uint8, device="cuda")  # a quarter
+    rows = torch.randint(-2, 3, (n, H), device="cuda", generator=g).to(torch.bfloat16)
+    out = product(rows, [n], [0, n], T, k, q, s, act)
+    table = torch.from_numpy(ref.E2M1.astype(np.float32)).cuda() / 4
+    y = torch.zeros(n, N, device="cuda")  # every sum is exact in float32
+    for i in range(H // 2):
+        code = q[0, :, i].int()
+        y += rows[:, 2 * i, None].float() * table[code & 15]
+        y += rows[:, 2 * i + 1, None].float() * table[code >> 4]
+    if act:
+        gate, up = y[:, :N // 2].double(), y[:, N // 2:].double()
+        want = gate * torch.sigmoid(gate) * up
+        # the gate's exponential and quotient, two products, and the output's half step
+        bound = want.abs() * (2.0 ** -8 + 16 * ULP * (1 + gate.abs())) + 1e-37
+        assert bool(((out.double() - want).abs() <= bound).all())
+    else:
+        assert torch.equal(out, y.to(torch.bfloat16))
