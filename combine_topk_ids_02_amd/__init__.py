@@ -1,5 +1,5 @@
-"""Python binding of libmoe_dispatch.so (MoE token dispatch and combine on
-MI355X / gfx950).
+"""Python binding of libmoe_dispatch.so (MoE routing, token dispatch, expert
+products and combine on MI355X / gfx950).
 
 Argument marshalling only: every step runs in the library's HIP kernels on the
 caller's current torch stream. Torch tensors supply device memory; bf16 rows

@@ -26,7 +26,8 @@
  *    argument error no kernel is launched.
  *  - Data-dependent errors are OR-ed by the kernels into `*err_word` (a device
  *    int32 the caller zeroes and reads when it chooses; may be NULL to ignore):
- *    MOE_ERRBIT_BAD_ID, MOE_ERRBIT_RANK_CAP, MOE_ERRBIT_EXPERT_CAP. Offending
+ *    MOE_ERRBIT_BAD_ID, MOE_ERRBIT_RANK_CAP, MOE_ERRBIT_EXPERT_CAP and, from
+ *    the router calls, MOE_ERRBIT_BAD_LOGIT, MOE_ERRBIT_BAD_SEQ. Offending
  *    rows are dropped, never written out of bounds ([A2A] sec 4.3: a batch
  *    larger than the cap fails).
  *  - Types: expert ids int32; weights float32; hidden states and expert
