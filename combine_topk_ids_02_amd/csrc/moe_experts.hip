@@ -101,6 +101,13 @@ __device__ __forceinline__ int run_of(const ProductArgs& a, int e, int64_t* firs
   return ((begin < 0) | (held <= 0)) ? 0 : int(held);
 }
 
+// Chunks of an expert; one (without rows) where the buffer holds none of its
+// rows, for the workgroup that takes it to say so.
+template <int kRows>
+__device__ __forceinline__ int chunks_of(int run, bool over) {
+  return run / kRows + (run % kRows > 0 || (run == 0 && over) ? 1 : 0);
+}
+
 // The chunk of at most kRows rows that an index stands for, found by a wave
 // looking at 64 experts at a time: an expert's first chunk (`beyond` false), or
 // one of those it has beyond its first. False when there are no more.
@@ -117,7 +124,7 @@ __device__ __forceinline__ bool chunk_of(const ProductArgs& a, bool beyond, int 
     int64_t first;
     bool over;
     const int run = run_of(a, min(e0 + lane, a.E - 1), &first, &over);
-    int n = run / kRows + (run % kRows > 0 ? 1 : 0);
+    int n = chunks_of<kRows>(run, over);
     n = e0 + lane >= a.E ? 0 : beyond ? max(0, n - 1) : min(1, n);
     int before = n;  // becomes the sum over the lanes up to this one
     for (int s = 1; s < kWave; s <<= 1) {

@@ -202,3 +202,24 @@ def test_widest_product(T, k, act):
         assert bool(((out.double() - want).abs() <= bound).all())
     else:
         assert torch.equal(out, y.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("counts,cap,T,k", [([1] * 6 + [0] * 42, 3, 1, 6),
+                                            ([0] * 40 + [2] * 8, 0, 4, 4),
+                                            ([80, 0, 90, 100], 80, 300, 1),
+                                            ([20, 0, 30, 7], 50, 60, 1)])
+def test_experts_past_the_buffer(counts, cap, T, k):
+    """Experts whose rows all lie past the buffer's end are flagged too."""
+    E, H, N = len(counts), 64, 32
+    g = torch.Generator(device="cuda")
+    g.manual_seed(8)
+    q = torch.randint(0, 256, (E, N, H // 2), dtype=torch.uint8, device="cuda", generator=g)
+    s = torch.full((E, N, 2), 127, dtype=torch.uint8, device="cuda")
+    rows = torch.randn(cap, H, device="cuda", generator=g).to(torch.bfloat16)
+    out = torch.zeros(cap, N, dtype=torch.bfloat16, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    moe.expert_product("mxfp4", rows, torch.tensor(counts, dtype=torch.int32, device="cuda"), off,
+                       T, k, q, s, out, err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == moe.ERRBIT_EXPERT_CAP
