@@ -21,11 +21,11 @@
 //    straight into registers they took 64 cache accesses an instruction (one
 //    per lane) and bounded the kernel: 190 us at that size.
 // Measured (kernel time; E = 48): one token's 6 experts, H = 5120, N = 4096,
-// SwiGLU, MXFP4 (67 MB) 16 us; 64 tokens in NVFP4 (566 MB) 128 us, 4.4 TB/s; H = 2048,
-// N = 5120 in MXFP4 (267 MB) 64 us, 4.2 TB/s; 256 tokens top-8 of E = 32, H =
-// 7168, N = 4096 in MXFP4 (499 MB, 64 rows an expert) 200 us. A kernel that only reads the codes
-// in this pattern takes 86 us and 47 us at the second and third size (5.9 and
-// 5.3 TB/s).
+// SwiGLU, MXFP4 (67 MB) 15 us; 64 tokens in NVFP4 (566 MB) 127 us, 4.5 TB/s; H =
+// 2048, N = 5120 in MXFP4 (267 MB) 63 us, 4.2 TB/s; 256 tokens top-8 of E = 32, H =
+// 7168, N = 4096 in MXFP4 (499 MB, 64 rows an expert) 179 us, up to 198 us in long
+// runs, where the clock falls. A kernel that only reads the codes in this
+// pattern takes 86 us and 47 us at the second and third size (5.9 and 5.3 TB/s).
 
 #include "moe_common.h"
 
@@ -166,13 +166,10 @@ __device__ __forceinline__ int offset_if(bool in, int off) {
   return r;
 }
 
-// What a wave takes of one granule of H (256 values): two loads of codes per
-// tile of 16 weight rows (lane (m, kq): row m, chunks kq and 4 + kq) and its
-// part of the granule of the buffer's rows.
-template <int NX>
-struct Stage {
+// What a wave takes of one granule of H (256 values) from the codes: two loads
+// per tile of 16 weight rows (lane (m, kq): row m, chunks kq and 4 + kq).
+struct Codes {
   vec4 code[2][NT];
-  vec4 x[NX];
 };
 
 // Scales: 128 bytes of each of the wave's weight rows at a time, a cache
@@ -206,7 +203,13 @@ __global__ __launch_bounds__(W * kWave, MT == 1 ? 3 : 2) void product_rows(Produ
   constexpr int kSuper = 128 / kPerGranule;              // granules whose scales are in LDS
   constexpr int NS = NT * kTile / 8;                     // 16-byte loads of them per lane
   static_assert(kSuper % kDepth == 0, "scales are renewed between rounds of the ring");
-  static_assert(kDepth % 2 == 0, "a granule of the ring has a slot of the two");
+  static_assert(kDepth == 2, "a granule of the ring has a slot of the two");
+  // Rows come to LDS in the middle of the granule before: with many of them the
+  // MFMAs hide the write and the wait for it (E = 48, H = 5120, N = 4096 in
+  // MXFP4, 16 rows an expert 148 -> 138 us, 64 rows 252 -> 226 us; H = 2048, N = 5120
+  // in NVFP4 103 -> 97 and 176 -> 169 us), with few the rows' loads would have
+  // too little time (8 rows 130 -> 143 us and, in MXFP4, 64 -> 80 us).
+  constexpr bool kHalfway = MT >= 2;
   __shared__ __align__(16) char staged[2 * (WK == 1 ? 1 : W) * kSlot];
   __shared__ __align__(16) uint8_t scales[W][NT * kTile * kScaleRow];
   __shared__ float part[WK == 1 ? 1 : W][NT * 4][WK == 1 ? 1 : kWave];
@@ -259,20 +262,31 @@ __global__ __launch_bounds__(W * kWave, MT == 1 ? 3 : 2) void product_rows(Produ
       const int64_t row0 = first + r0;
       const buffer xb = make_buffer(a.rows + row0 * a.K, nr * a.K * 2);
 
-      // The loads of a stage stay together and in the order of the stages: a
-      // wait for one stage then leaves the later ones on their way.
-      auto load = [&](Stage<NX>& f, int s) {
+      // Loads stay together and in the order of the granules: a wait for one
+      // then leaves the later ones on their way.
+      auto load_rows = [&](vec4 (&xr)[NX], int s) {
         __builtin_amdgcn_sched_barrier(0);
         const int g = g0 + s;
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
           const int r = (sharer + i * kSharers) >> 5, p = 32 * g + (sharer & 31);
           const int off = offset_if(p < 4 * end, r * (a.K * 2) + p * 16);
-          f.x[i] = __builtin_bit_cast(vec4, __builtin_amdgcn_raw_buffer_load_b128(xb, off, 0, 0));
+          xr[i] = __builtin_bit_cast(vec4, __builtin_amdgcn_raw_buffer_load_b128(xb, off, 0, 0));
         }
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      auto store_rows = [&](const vec4 (&xr)[NX], char* at) {
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+          const int r = (sharer + i * kSharers) >> 5, p = sharer & 31;
+          *reinterpret_cast<vec4*>(at + piece_at(r, p)) = xr[i];
+        }
+      };
+      auto load_codes = [&](Codes& f, int s) {
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int c = 8 * g + 4 * u + kq;
+          const int c = 8 * (g0 + s) + 4 * u + kq;
           const int off = offset_if(c < end, m * (a.K / 2) + c * 16);
 #pragma unroll
           for (int h = 0; h < NT; ++h)
@@ -320,47 +334,69 @@ __global__ __launch_bounds__(W * kWave, MT == 1 ? 3 : 2) void product_rows(Produ
         __builtin_amdgcn_wave_barrier();
       };
 
-      // kDepth granules are on their way at any time. One past the last reads
-      // nothing and adds 0.
-      Stage<NX> f[kDepth];
-      load_scales(0);
+      // The scales of this lane's chunk 4 u + kq of a granule, 0 past H (a code
+      // there is 0, but 0 times a NaN scale would not be).
+      auto read_scales = [&](uint32_t (&v)[NT], int s, int u) {
 #pragma unroll
-      for (int d = 0; d < kDepth; ++d) load(f[d], d);
+        for (int h = 0; h < NT; ++h) {
+          const uint8_t* p = sc + (h * kTile + m) * kScaleRow + (s % kSuper) * kPerGranule;
+          const uint32_t byte = kE4M3 ? *reinterpret_cast<const uint16_t*>(p + 8 * u + 2 * kq)
+                                      : p[4 * u + kq];
+          v[h] = 8 * (g0 + s) + 4 * u + kq < end ? byte : 0;
+        }
+      };
+      auto wait_for_all = [&]() {
+        if (WK == 1)
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        else
+          __builtin_amdgcn_wave_barrier();
+      };
+
+      // kDepth granules are on their way at any time. One past the last reads
+      // nothing and adds 0. The rows of a granule come to LDS as it begins, or
+      // (kHalfway) in the middle of the one before, into the slot that was last
+      // read before that one's barrier, and its scales to registers.
+      Codes f[kDepth];
+      vec4 xr[kHalfway ? 1 : kDepth][NX];  // this thread's parts of granules of the rows
+      uint32_t b[2][NT], next[2][NT];
+      load_scales(0);
+      load_rows(xr[0], 0);
+      load_codes(f[0], 0);
+      if (kHalfway) {
+        store_scales(0);
+        read_scales(b[0], 0, 0);
+        read_scales(b[1], 0, 1);
+        store_rows(xr[0], lds);
+      }
+      load_rows(xr[kHalfway ? 0 : 1], 1);
+      load_codes(f[1], 1);
       f32x4 acc[NT][MT];
 #pragma unroll
       for (int h = 0; h < NT; ++h)
 #pragma unroll
         for (int q = 0; q < MT; ++q) acc[h][q] = f32x4{0, 0, 0, 0};
+      if (kHalfway) wait_for_all();
       for (int s0 = 0; s0 < stages; s0 += kDepth) {
-        if (s0 % kSuper == 0) store_scales(s0);
-        if ((s0 + kDepth) % kSuper == 0) load_scales(s0 + kDepth);
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) {
           const int s = s0 + d;
-          // The granule's rows to LDS, two slots in turn: the one written here
-          // was last read before the barrier of the granule before.
           char* at = lds + d % 2 * kSlot;
-#pragma unroll
-          for (int i = 0; i < NX; ++i) {
-            const int r = (sharer + i * kSharers) >> 5, p = sharer & 31;
-            *reinterpret_cast<vec4*>(at + piece_at(r, p)) = f[d].x[i];
+          if (!kHalfway) {
+            if (d == 0 && s % kSuper == 0) store_scales(s);
+            if (d == 0 && (s + kDepth) % kSuper == 0) load_scales(s + kDepth);
+            store_rows(xr[d], at);
+            wait_for_all();
           }
-          if (WK == 1)
-            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-          else
-            __builtin_amdgcn_wave_barrier();
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            // this lane's chunk: its scale, 0 past H (a code there is 0, but
-            // 0 times a NaN scale would not be)
-            const bool in = 8 * (g0 + s) + 4 * u + kq < end;
-            uint32_t b[NT];
-#pragma unroll
-            for (int h = 0; h < NT; ++h) {
-              const uint8_t* p = sc + (h * kTile + m) * kScaleRow + (s % kSuper) * kPerGranule;
-              const uint32_t v = kE4M3 ? *reinterpret_cast<const uint16_t*>(p + 8 * u + 2 * kq)
-                                       : p[4 * u + kq];
-              b[h] = in ? v : 0;
+            if (!kHalfway) read_scales(b[u], s, u);
+            if (kHalfway && u == 1) {
+              store_rows(xr[0], lds + (d + 1) % 2 * kSlot);
+              if (d == 1 && (s + 1) % kSuper == 0) store_scales(s + 1);
+              if (d == 0 && (s + 2) % kSuper == 0) load_scales(s + 2);
+              load_rows(xr[0], s + 2);
+              read_scales(next[0], s + 1, 0);
+              read_scales(next[1], s + 1, 1);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -375,10 +411,10 @@ __global__ __launch_bounds__(W * kWave, MT == 1 ? 3 : 2) void product_rows(Produ
                 const uint32_t code = f[d].code[u][h][j];
                 bf16x8 w;
                 if (kE4M3)
-                  w = expand_e4m3(code, j < 2 ? __builtin_amdgcn_cvt_f32_fp8(b[h], 0)
-                                              : __builtin_amdgcn_cvt_f32_fp8(b[h], 1));
+                  w = expand_e4m3(code, j < 2 ? __builtin_amdgcn_cvt_f32_fp8(b[u][h], 0)
+                                              : __builtin_amdgcn_cvt_f32_fp8(b[u][h], 1));
                 else
-                  w = expand_e8m0(code, __uint_as_float(b[h] << 23));
+                  w = expand_e8m0(code, __uint_as_float(b[u][h] << 23));
 #pragma unroll
                 for (int q = 0; q < MT; ++q) {
                   acc[h][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x[q], acc[h][q], 0, 0, 0);
@@ -386,7 +422,15 @@ __global__ __launch_bounds__(W * kWave, MT == 1 ? 3 : 2) void product_rows(Produ
               }
             }
           }
-          load(f[d], s + kDepth);
+          if (!kHalfway) load_rows(xr[d], s + kDepth);
+          load_codes(f[d], s + kDepth);
+          if (kHalfway) {
+            wait_for_all();
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int h = 0; h < NT; ++h) b[u][h] = next[u][h];
+          }
         }
       }
 
@@ -408,7 +452,7 @@ __global__ __launch_bounds__(W * kWave, MT == 1 ? 3 : 2) void product_rows(Produ
             for (int i = 0; i < 4; ++i)
               put(q * kTile + m, h, i, acc[h][q][i] * factor, acc[(h + 1) % NT][q][i] * factor);
         // LDS is written anew when every wave is done with it
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (!kHalfway) wait_for_all();
       } else {
         // join the waves' parts: thread (wave i, lane) adds up element i of
         // every fragment of that lane, in wave order
@@ -460,16 +504,17 @@ int column_tiles(int form, bool swiglu, int wide) {
 // By the mean number of rows of an expert that has any (uniform routing at
 // worst): as many rows at a time as that takes, since every chunk of rows
 // reads the codes again. Measured at E = 48, H = 5120, N = 4096 with SwiGLU in
-// MXFP4, mean rows 2 / 6 / 8 / 12 / 24 / 32: 16 rows 80 / 101 / 113 / 130 /
-// 195 / 236 us, 32 rows 102 / 109 / 110 / 123 / 152 / 183 us, 64 rows 122 /
-// 126 / 130 / 133 / 152 / 171 us (H = 2048, N = 5120 in NVFP4 alike).
+// MXFP4, mean rows 2 / 8 / 12 / 16 / 20 / 24 / 32: 16 rows 75 / 113 / 130 / 158 / 175 /
+// 193 / 236 us, 32 rows 90 / 107 / 128 / 138 / 142 / 149 / 177 us, 64 rows 100 / 121 / 123 /
+// 140 / 149 / 142 / 160 us; H = 2048, N = 5120 in NVFP4: 55 / 76 / 86 / 102 / 113 / 123 / 152,
+// 69 / 82 / 82 / 97 / 101 / 107 / 130 and 77 / 91 / 93 / 97 / 100 / 103 / 122 us.
 // Few workgroups with long rows split H over the waves instead of columns:
 // 16.3 against 18.6 us for one token's 6 experts there (192 workgroups), 27
 // against 30 us for two tokens', but 49.1 against 49.2 us for four (768), and
 // at H = 2048 14.8 against 14.3 us for one.
 int form_of(const moe_shape_t& sh, bool swiglu, int wide, int64_t pairs, int64_t active) {
   const int64_t mean = (pairs + active - 1) / active;
-  if (mean > 24) return 3;
+  if (mean > 20) return 3;
   if (mean > 10) return 2;
   const bool few = active * column_tiles(1, swiglu, wide) < 512;
   return mean <= 2 && few && sh.H >= 4096 ? 0 : 1;
