@@ -9,6 +9,7 @@ import torch
 import combine_topk_ids_02_amd as moe
 import router_ref as ref
 from router_ref import ULP
+from test_experts_gpu import check
 
 pytestmark = pytest.mark.gpu
 
@@ -223,3 +224,18 @@ def test_experts_past_the_buffer(counts, cap, T, k):
                        T, k, q, s, out, err=err)
     torch.cuda.synchronize()
     assert int(err.item()) == moe.ERRBIT_EXPERT_CAP
+
+
+# counts, H, N, act: every number of rows at a time, with scales renewed within
+# a row (past H = 2048 in NVFP4, 4096 in MXFP4) and H that ends inside a granule
+LONG_ROWS = [([3, 1], 4640, 40, None), ([14, 18], 2080, 96, "swiglu"), ([14, 18], 8224, 40, None),
+             ([33, 0, 5, 20], 4128, 66, "swiglu"), ([70, 10, 65], 4384, 80, None),
+             ([129, 1], 8480, 40, "swiglu"), ([64, 16, 48], 6176, 300, None)]
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("case", range(len(LONG_ROWS)))
+def test_product_long_rows(fmt, case):
+    say(f"[long rows] {fmt} {LONG_ROWS[case]}")
+    counts, H, N, act = LONG_ROWS[case]
+    check(fmt, counts, H, N, act, case % 2 == 0, seed=60 + case)
