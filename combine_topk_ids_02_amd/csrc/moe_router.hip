@@ -689,7 +689,7 @@ constexpr int kTileWaves = kTileThreads / kWave;
 // slot tile + sequence (increasing along the tokens, so no two pairs of them
 // share one) and start anew. Bound by latency: T = 16384, E = 256 with
 // sigmoids of bfloat16 logits (8.4 MB) takes 9.6 us (23.7 us with a wave per
-// token), T = 4096, E = 384 in float32 5.8 us.
+// token), T = 4096, E = 384 in float32 6.7 us.
 template <typename Tz, int LT, int V, bool kSigmoid, bool kFull>
 __global__ __launch_bounds__(kTileThreads) void balance_tiles(BalanceArgs a) {
   extern __shared__ float lds_all[];
@@ -762,8 +762,9 @@ __global__ __launch_bounds__(kTileThreads) void balance_tiles(BalanceArgs a) {
 // slices-th tile, then the slices are joined, all in an order that the sizes
 // alone fix and in 64 bits. (A workgroup per 64 experts, the last of them
 // adding up the loss, took 7.3 us for 13 sequences of 16384 tokens where this
-// takes 5.7, and 7.5 against 7.8 us for one of 4096: the fence and the count
-// between workgroups cost what reading from more of them gave.)
+// takes 5.7, and with 128 tiles 7.5 against 7.8 us for one of 4096, which takes
+// 5.7 with 64: the fence and the count between workgroups cost what reading from
+// more of them gave.)
 constexpr int kJoinThreads = 1024;
 constexpr int kJoinSlices = 32;  // at most
 __global__ __launch_bounds__(kJoinThreads) void balance_join(BalanceArgs a) {
@@ -1129,13 +1130,15 @@ void by_type_tokens(int type, int E, Args&&... args) {
   return by_tokens<F, _Float16>(E, args...);
 }
 
-// Tiles of the balance loss: at most 256, of a multiple of 32 tokens (a
-// workgroup's pass).
+// Tiles of the balance loss: a multiple of 32 tokens (a workgroup's pass), at
+// most 256 of them; two passes rather than more than 64 tiles, for the join
+// reads every tile of a sequence (T = 4096, E = 384: 64 tiles 6.7 + 5.9 us, 128 tiles
+// 5.8 + 7.8 us, 32 tiles 10.1 + 5.1 us).
 constexpr int kMaxTiles = 256;
 constexpr int kPass = kTileWaves * 4;
 int balance_tile(int T) {
   const int least = (T + kMaxTiles - 1) / kMaxTiles;
-  return std::max(1, (least + kPass - 1) / kPass) * kPass;
+  return std::max(T > 64 * kPass ? 2 : 1, (least + kPass - 1) / kPass) * kPass;
 }
 int balance_tile_count(int T) {
   const int tile = balance_tile(T);
