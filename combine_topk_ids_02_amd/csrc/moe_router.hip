@@ -374,9 +374,9 @@ __global__ __launch_bounds__(kBlock) void route_tokens(RouteArgs a) {
 
   if (kKeyed && a.groups > 1) {
     // Group g is the registers [g * per, (g + 1) * per): the two largest keys of
-    // every group, its score in lane g of the row.
+    // every group, in the end in lane g of the row.
     const int per = E / a.groups / 16;
-    int score_key = kAbsent;         // lane g: the group's score, as a key
+    int first_key = kAbsent, second_key = kAbsent;  // lane g: those of group g
     int x = kAbsent, y = kAbsent;    // the two largest so far
     int g = 0, left = per;
 #pragma unroll
@@ -388,43 +388,54 @@ __global__ __launch_bounds__(kBlock) void route_tokens(RouteArgs a) {
         merge_two<kRowRor + 4>(x, y);
         merge_two<kRowRor + 2>(x, y);
         merge_two<kRowRor + 1>(x, y);
-        const int score = y >= kLeast ? ordered(unordered(x) + unordered(y)) : x;
-        if (l == g) score_key = score;
+        if (l == g) {
+          first_key = x;
+          second_key = y;
+        }
         x = y = kAbsent;
         ++g;
         left = per;
       }
     }
-    int head = l < a.groups ? score_key : kAbsent;
+    // A sigmoid here is off by at most 2^-22 (4 roundings), a key by that and two
+    // roundings of its size, a score by both keys' and two of its own: 4.8e-7 and
+    // 2^-22 of the keys' sizes, which their sum says nothing of where they cancel.
+    // `off` is twice that (products first: it cannot overflow).
+    const float one = unordered(first_key);
+    const float two = second_key >= kLeast ? unordered(second_key) : 0.0f;
+    const float score = one + two;
+    const float off = first_key >= kLeast ? 1e-6f + (fabsf(one) * 0x1p-21f + fabsf(two) * 0x1p-21f)
+                                          : 0.0f;
+    int head = first_key >= kLeast ? ordered(score) : kAbsent;  // as a key
     // the best top_groups of them, the first of equal ones: lane g learns
-    // whether its group is kept, and all lanes the last kept and the first not
+    // whether its group is kept
     bool kept = false;
-    int worst = kAbsent;
-    uint64_t at_worst = 0;
     for (int r = 0; r < a.top_groups; ++r) {
-      worst = row_max_int(head);
-      at_worst = first_of_rows(head == worst);
+      const int worst = row_max_int(head);
+      const uint64_t at_worst = first_of_rows(head == worst);
       if (((at_worst >> lane) & 1) && head >= kLeast) {
         kept = true;
         head = kAbsent;
       }
     }
-    // a sigmoid here is off by at most 2^-22 (4 roundings), a score by twice that
-    // and its roundings, two scores by twice that
-    const int next = row_max_int(head);
-    const float slack = 2e-6f + fabsf(unordered(worst)) * 0x1p-21f;
-    const bool close = next >= kLeast && unordered(worst) - unordered(next) < slack;
+    // A kept group can be exactly below one that is not only where the least it
+    // may score is not above the most the other may. (Scores past 2^127 count as
+    // that, which leaves room for `off`.)
+    const float score_at = fminf(fmaxf(score, -0x1p127f), 0x1p127f);
+    const float least = score_at - off;
+    const float most = off > 0.0f ? score_at + off : -INFINITY;
+    const float worst = -row_max(kept ? -least : -INFINITY);
+    const float next = row_max(kept ? -INFINITY : most);
+    const bool close = worst <= next;
     if (__ballot(close && routed)) {
-      // exact scores of the two groups decide; a third as close goes the long way
-      const uint64_t at_next = first_of_rows(head == next);
-      const int group_a = __ffs(int(at_worst >> (lane & 48) & 0xFFFF)) - 1;
-      const int group_b = __ffs(int(at_next >> (lane & 48) & 0xFFFF)) - 1;
-      const int third = row_max_int(l == group_b ? kAbsent : head);
-      unsure |= close && third >= kLeast && unordered(worst) - unordered(third) < slack;
-      int before = l < a.groups && kept && l != group_a ? ordered(-unordered(score_key)) : kAbsent;
-      before = row_max_int(before);  // the last but one kept, negated
-      unsure |= close && before >= kLeast && -unordered(before) - unordered(next) < slack;
-      float score[2];
+      // exact scores decide between one such kept group and one such other; more
+      // of either go the long way
+      const uint32_t doubted = uint32_t(__ballot(kept && least <= next) >> (lane & 48)) & 0xFFFF;
+      const uint32_t hopeful = uint32_t(__ballot(!kept && most >= worst) >> (lane & 48)) & 0xFFFF;
+      unsure |= close && (__popc(doubted) != 1 || __popc(hopeful) != 1);
+      const int group_a = max(__ffs(int(doubted)) - 1, 0);
+      const int group_b = max(__ffs(int(hopeful)) - 1, 0);
+      float exact[2];
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         int x2 = kAbsent, y2 = kAbsent;
@@ -440,9 +451,9 @@ __global__ __launch_bounds__(kBlock) void route_tokens(RouteArgs a) {
         merge_two<kRowRor + 4>(x2, y2);
         merge_two<kRowRor + 2>(x2, y2);
         merge_two<kRowRor + 1>(x2, y2);
-        score[w] = y2 >= kLeast ? unordered(x2) + unordered(y2) : unordered(x2);
+        exact[w] = y2 >= kLeast ? unordered(x2) + unordered(y2) : unordered(x2);
       }
-      const bool swap = score[1] > score[0] || (score[1] == score[0] && group_b < group_a);
+      const bool swap = exact[1] > exact[0] || (exact[1] == exact[0] && group_b < group_a);
       if (close && swap) kept = l == group_b || (kept && l != group_a);
     }
     const uint32_t keep = uint32_t(__ballot(kept) >> (lane & 48));
