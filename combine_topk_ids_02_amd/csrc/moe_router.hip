@@ -241,8 +241,9 @@ __device__ __forceinline__ void merge_two(int& x, int& y) {
 }
 
 // Floats as integers of the same order (-0 as +0). Below kLeast lie -infinity
-// and kAbsent: no key.
+// (kNone) and kAbsent: no key.
 constexpr int kAbsent = INT32_MIN;
+constexpr int kNone = int(0x807FFFFFu);
 constexpr int kLeast = int(0x80800000u);  // the lowest finite float
 __device__ __forceinline__ int ordered(float v) {
   const int b = __float_as_int(v + 0.0f);
@@ -406,14 +407,17 @@ __global__ __launch_bounds__(kBlock) void route_tokens(RouteArgs a) {
     const float score = one + two;
     const float off = first_key >= kLeast ? 1e-6f + (fabsf(one) * 0x1p-21f + fabsf(two) * 0x1p-21f)
                                           : 0.0f;
-    int head = first_key >= kLeast ? ordered(score) : kAbsent;  // as a key
+    // The score as a key. Two keys may sum to -infinity, which is the score of a
+    // group without any too: it takes part all the same.
+    int head = first_key >= kLeast ? ordered(score) : kNone;
+    if (l >= a.groups) head = kAbsent;
     // the best top_groups of them, the first of equal ones: lane g learns
     // whether its group is kept
     bool kept = false;
     for (int r = 0; r < a.top_groups; ++r) {
       const int worst = row_max_int(head);
       const uint64_t at_worst = first_of_rows(head == worst);
-      if (((at_worst >> lane) & 1) && head >= kLeast) {
+      if ((at_worst >> lane) & 1) {  // a group's: there are top_groups of them
         kept = true;
         head = kAbsent;
       }
@@ -438,12 +442,12 @@ __global__ __launch_bounds__(kBlock) void route_tokens(RouteArgs a) {
       float exact[2];
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        int x2 = kAbsent, y2 = kAbsent;
+        int x2 = kNone, y2 = kNone;
         for (int i = 0; i < per; ++i) {
           const int e = min((w ? group_b : group_a) * per * 16 + i * 16 + l, E - 1);
           const float ze = float(row[e]);
           const float ke = sigmoid_nearest(ze) + (a.bias ? a.bias[e] : 0.0f);
-          const int o = ze == -INFINITY ? kAbsent : ordered(ke);
+          const int o = ze == -INFINITY ? kNone : ordered(ke);
           y2 = max(y2, min(x2, o));
           x2 = max(x2, o);
         }

@@ -475,9 +475,10 @@ typedef struct moe_router {
  *   addition). The k largest keys are chosen, largest first, equal keys by the
  *   lower id. With groups > 1 only the experts of the best top_groups groups
  *   take part: a group's score is the sum of its two largest keys (its only
- *   key where it has one), equal scores by the lower group. The weights are
- *   made from the scores (the bias is not in them): scale * s_e, or scale *
- *   s_e over the sum of the token's chosen scores (renorm).
+ *   key where it has one; -infinity where it has none or its two sum to that),
+ *   equal scores by the lower group. The weights are made from the scores (the
+ *   bias is not in them): scale * s_e, or scale * s_e over the sum of the
+ *   token's chosen scores (renorm).
  *   An expert whose key is -infinity is never chosen; slots without an expert
  *   get id -1 and weight 0. A token with a NaN or +infinite logit or key is
  *   given no expert and flagged (MOE_ERRBIT_BAD_LOGIT).

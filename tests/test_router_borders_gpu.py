@@ -75,3 +75,65 @@ def test_group_scores_that_cancel(E, groups, top, size, kind):
     got = choose(z, 2 * top, moe.Router("sigmoid", True, 1.0, groups, top), bias)
     wrong = np.nonzero((got != want).any(axis=1))[0]
     assert wrong.size == 0, (wrong.size, wrong[:5], got[wrong[:3]], want[wrong[:3]])
+
+
+LOWEST = np.float32(-3.4028234663852886e38)
+
+
+@pytest.mark.parametrize("E,groups", [(64, 4), (60, 4), (256, 8), (250, 5), (48, 3)])
+def test_groups_barred_by_the_lowest_bias(E, groups):
+    """A bias of float32's lowest value bars experts without removing them: two
+    such keys sum to -infinity, but their group takes part behind the others (as
+    one whose keys are all -infinity does, the lower of equal groups first)."""
+    rng = np.random.default_rng(E)
+    T, per = 60, E // groups
+    for top in range(1, groups + 1):
+        for barred in ("all", "groups", "most", "one group", "half"):
+            bias = (rng.normal(size=E) * 0.1).astype(np.float32)
+            bias = bias.reshape(groups, per)
+            if barred == "all":
+                bias[:] = LOWEST
+            elif barred == "groups":  # all but one group
+                bias[np.arange(groups) != groups // 2] = LOWEST
+            elif barred == "most":    # one expert left in each, none in the first
+                bias[:, 1:] = LOWEST
+                bias[0] = LOWEST
+            elif barred == "one group":
+                bias[0] = LOWEST
+            else:
+                bias[rng.random((groups, per)) < 0.5] = LOWEST
+            bias = bias.reshape(E)
+            z = rng.normal(size=(T, E)).astype(np.float32)
+            zg = z.reshape(T, groups, per)
+            zg[10:20, 0] = -np.inf          # a group without any key, before barred ones
+            zg[20:30, 1:] = -np.inf         # only the first group has keys
+            zg[30:35, : groups - 1] = -np.inf
+            zg[35:40, :, : per - 1] = -np.inf  # one key a group
+            for k in (3, 8):
+                say(f"[barred] E={E} groups={groups} top={top} {barred} k={k}")
+                want, flagged = ref.choose(z, k, "sigmoid", bias, groups, top)
+                assert not flagged
+                got = choose(z, k, moe.Router("sigmoid", True, 1.0, groups, top), bias)
+                assert np.array_equal(got, want), (np.nonzero((got != want).any(axis=1))[0],)
+
+
+def test_groups_next_to_the_ends_of_float32():
+    """Scores that overflow to either infinity, or just do not."""
+    rng = np.random.default_rng(3)
+    T, E, groups = 200, 64, 4
+    for big in (1.7014117e38, 1.7014118e38, 1.7014120e38, 3.0e38, 3.4e38):
+        for sign in (1.0, -1.0):
+            bias = np.full((groups, 16), -LOWEST * np.float32(-0.5), np.float32)
+            bias += (rng.integers(-3, 4, size=bias.shape) * 2.0 ** 103).astype(np.float32)
+            bias[:, :2] = np.float32(sign * big)
+            if sign < 0:
+                bias[:, 2:] = LOWEST
+            bias[1, 0] = np.nextafter(bias[1, 0], np.float32(0))
+            bias[2, 1] = np.nextafter(bias[2, 1], np.float32(0))
+            bias = bias.reshape(E)
+            z = rng.normal(size=(T, E)).astype(np.float32)
+            for top in (1, 2, 3):
+                want, flagged = ref.choose(z, 6, "sigmoid", bias, groups, top)
+                assert not flagged
+                got = choose(z, 6, moe.Router("sigmoid", True, 1.0, groups, top), bias)
+                assert np.array_equal(got, want), (big, sign, top)
