@@ -633,6 +633,16 @@ __device__ __forceinline__ void shares(const float (&z)[V], float (&p)[V], float
         inner[i] = 1.0f;
       }
   }
+  if (__ballot(fabsf(m) > 0x1p20f)) {
+    // The rounding of `top` is a factor on all of a token's exponentials, from
+    // here on no longer near 1: it passes float32's range at |m| = 2^32, as m
+    // log2 e does at the end of it. There the difference comes first, which
+    // costs it a rounding (and sigmoids of logits above are ones as they stand).
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (fabsf(m) > 0x1p20f && !(kSigmoid && m > 0.0f))
+        p[i] = __builtin_amdgcn_exp2f((z[i] - m) * kLog2e);
+  }
 #pragma unroll
   for (int i = 0; i < V; ++i) sum += p[i];
   sum = token_sum<LT>(sum);

@@ -137,3 +137,96 @@ def test_groups_next_to_the_ends_of_float32():
                 assert not flagged
                 got = choose(z, 6, moe.Router("sigmoid", True, 1.0, groups, top), bias)
                 assert np.array_equal(got, want), (big, sign, top)
+
+
+def far_rows(E, dtype):
+    """Logits near the ends of the type, one kind a row, all finite or masked."""
+    info = torch.finfo(dtype)
+    rng = np.random.default_rng(17)
+    z = torch.from_numpy(rng.normal(size=(64, E)).astype(np.float32)).to(dtype)
+    z[0] = info.min                      # all lowest: even shares
+    z[1] = info.min
+    z[1, 3] = -1.0                       # one share
+    z[2] = info.min
+    z[2, 5:] = -float("inf")             # five shares
+    z[3] = info.max
+    z[4, 7] = info.max                   # one share, or (sigmoid) about even ones
+    z[5] = info.max * 0.75
+    z[5, 2:] = info.max * 0.5            # two shares
+    z[6] = info.min * 0.75
+    z[6, 4:] = info.min                  # four
+    z[7] = info.min * 0.25
+    z[7, 9] = info.min * 0.125
+    z[8] = info.max * 0.71               # about where log2(e) times it passes the end
+    z[9] = info.min * 0.71
+    z[10] = info.max * 0.68
+    z[11] = info.min * 0.68
+    z[12, :] = info.min
+    z[12, 6] = info.max
+    # 13: ordinary; behind it a step or some of the type apart, from 4 on up, of
+    # both signs (1.44 times such a logit is rounded by much more than 1)
+    for i in range(14, 64):
+        base = torch.tensor(3.0 * 2.0 ** (i - 13) * (-1) ** i).clamp(info.min / 2, info.max / 2)
+        base = base.to(dtype)
+        step = 2.0 ** torch.frexp(base.double().abs())[1] * info.eps / 2
+        near = torch.from_numpy(rng.integers(-3, 4, size=E))
+        z[i] = (base.double() + near * step).to(dtype)
+    return z
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [40, 64, 600])
+def test_shares_of_far_logits(dtype, scoring, E):
+    """The balance loss and the gradient where every logit of a token is finite
+    but as far out as its type goes."""
+    say(f"[far] {dtype} {scoring} E={E}")
+    z_d = far_rows(E, dtype).cuda()
+    z = z_d.double().cpu().numpy()
+    T, k = z.shape[0], 3
+    rng = np.random.default_rng(18)
+    ids = rng.integers(0, E, size=(T, k)).astype(np.int32)
+    ids[:, 0] = 3
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ids_d = torch.from_numpy(ids).cuda()
+    err = torch.zeros(1, **i32)
+    off = np.arange(T + 1)               # a sequence per row: its shares are its means
+    off_d = torch.arange(T + 1, **i32)
+    loss, mean = torch.full((T,), -7.0, device="cuda"), torch.full((T, E), -7.0, device="cuda")
+    counts, tokens = torch.full((T, E), -7, **i32), torch.full((T,), -7, **i32)
+    ws = torch.empty(moe.balance_workspace_bytes(T, E, k, T), dtype=torch.uint8, device="cuda")
+    moe.balance_loss(z_d, ids_d, moe.Router(scoring), loss, counts, tokens, mean, workspace=ws,
+                     seq_offsets=off_d, err=err)
+    torch.cuda.synchronize()
+    wl, wc, wt, wm = ref.balance(z, ids, scoring, off)
+    assert int(err.item()) == 0
+    assert np.array_equal(counts.cpu().numpy(), wc) and np.array_equal(tokens.cpu().numpy(), wt)
+    # a share: its exponential and argument (an exponent of at most 110, beyond
+    # it is 0), the sum over E and three single roundings
+    rel = (2 * 110 + E / 16 + 8) * ref.ULP
+    assert (abs(mean.double().cpu().numpy() - wm) <= wm * rel + 1e-37).all()
+    # a share below 2^-126 may be 0: each of the k pairs of the one token adds E / k
+    # times its expert's share, so a loss is off by at most E * 2^-126 for that
+    assert (abs(loss.double().cpu().numpy() - wl) <= wl * (rel + 2 * ref.ULP) +
+            E * 2.0 ** -126).all()
+
+    dw = rng.normal(size=(T, k)).astype(np.float32)
+    dl = rng.normal(size=T).astype(np.float32)
+    step, least = {torch.float32: (0.0, 0.0), torch.bfloat16: (2.0 ** -8, 0.0),
+                   torch.float16: (2.0 ** -11, 2.0 ** -25)}[dtype]
+    # and p (u - sum p u) with every p off by at most 2^-126: by 2^-126 of |u| and of
+    # sum |u| twice (|sum p u| <= sum |u|), where sum |u| <= |d_loss| E / k * (k + k)
+    # from the counts and k T' / E, and sum |d_weights| from the raw weights
+    flushed = 3 * 2.0 ** -126 * (2 * E * abs(dl) + abs(dw).sum(axis=1)).astype(np.float64)[:, None]
+    for renorm in (True, False):
+        dz = torch.full((T, E), -7.0, dtype=dtype, device="cuda")
+        moe.route_backward(z_d, ids_d, moe.Router(scoring, renorm), dz,
+                           d_weights=torch.from_numpy(dw).cuda(),
+                           balance=(torch.from_numpy(dl).cuda(), counts, tokens, off_d), err=err)
+        torch.cuda.synchronize()
+        want, size = ref.gradient(z, ids, scoring, renorm, 1.0, dw, dl, off)
+        got = dz.double().cpu().numpy()
+        assert int(err.item()) == 0 and np.isfinite(got).all()
+        # as above, the quotients and sums over k, then the output's half step
+        bound = (rel + (2 * k + 16) * ref.ULP) * size * (1 + step) + step * abs(want) + least + flushed
+        assert (abs(got - want) <= bound).all()
