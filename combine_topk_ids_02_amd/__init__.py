@@ -724,7 +724,8 @@ def route_backward(logits: torch.Tensor, topk_ids, router: Router, d_logits, *, 
 
 
 def balance_workspace_bytes(T: int, E: int, k: int, sequences: int = 1) -> int:
-    """moe_balance_workspace_bytes: scratch that balance_loss() needs."""
+    """moe_balance_workspace_bytes: scratch that balance_loss() needs, for this
+    many tokens, experts and sequences or fewer."""
     return int(lib().moe_balance_workspace_bytes(_sizes(T, 8, E, k), sequences))
 
 

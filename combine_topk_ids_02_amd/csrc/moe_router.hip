@@ -1156,25 +1156,35 @@ void by_type_tokens(int type, int E, Args&&... args) {
 }
 
 // Tiles of the balance loss: a multiple of 32 tokens (a workgroup's pass), at
-// most 256 of them; two passes rather than more than 64 tiles, for the join
+// most 256 of them; two passes where one would make more than 64 tiles, for the join
 // reads every tile of a sequence (T = 4096, E = 384: 64 tiles 6.7 + 5.9 us, 128 tiles
-// 5.8 + 7.8 us, 32 tiles 10.1 + 5.1 us).
+// 5.8 + 7.8 us, 32 tiles 10.1 + 5.1 us), and more only past 16384 tokens.
 constexpr int kMaxTiles = 256;
+constexpr int kOnePassTiles = 64;
 constexpr int kPass = kTileWaves * 4;
 int balance_tile(int T) {
   const int least = (T + kMaxTiles - 1) / kMaxTiles;
-  return std::max(T > 64 * kPass ? 2 : 1, (least + kPass - 1) / kPass) * kPass;
+  return std::max(T > kOnePassTiles * kPass ? 2 : 1, (least + kPass - 1) / kPass) * kPass;
 }
 int balance_tile_count(int T) {
   const int tile = balance_tile(T);
   return (T + tile - 1) / tile;
 }
 
-// The workspace: sums and pairs [slots * stride], used [slots].
-size_t balance_slots(const moe_shape_t& sh, int sequences) {
-  return size_t(balance_tile_count(sh.T)) + sequences;
+// The most tiles that any batch of up to T tokens has (a longer tile makes
+// fewer: 2048 tokens have 64, 2049 have 33, so a workspace for the second alone
+// would not do for the first).
+int balance_tile_bound(int T) {
+  return std::max(std::min((T + kPass - 1) / kPass, kOnePassTiles),
+                  std::min((T + 2 * kPass - 1) / (2 * kPass), kMaxTiles));
 }
+
+// The workspace: sums and pairs [slots * stride], used [slots], a slot for
+// every tile and sequence.
 int balance_stride(const moe_shape_t& sh) { return (sh.E + 3) / 4 * 4; }
+size_t balance_bytes(const moe_shape_t& sh, int tiles, int sequences) {
+  return (size_t(tiles) + sequences) * (size_t(balance_stride(sh)) * 8 + 4);
+}
 
 }  // namespace
 
@@ -1236,7 +1246,7 @@ int moe_route_backward(const moe_shape_t* shape, const moe_router_t* router, int
 
 size_t moe_balance_workspace_bytes(const moe_shape_t* shape, int sequences) {
   if (!shape_ok(shape) || sequences < 1 || sequences > kMaxSequences) return 0;
-  return balance_slots(*shape, sequences) * (size_t(balance_stride(*shape)) * 8 + 4);
+  return balance_bytes(*shape, balance_tile_bound(shape->T), sequences);
 }
 
 int moe_balance_loss(const moe_shape_t* shape, const moe_router_t* router, int logits_type,
@@ -1249,13 +1259,13 @@ int moe_balance_loss(const moe_shape_t* shape, const moe_router_t* router, int l
   if (!seq_offsets && sequences != 1) return MOE_ERR_ARG;
   if (!loss || !expert_counts || !token_counts || !score_mean || !workspace) return MOE_ERR_ARG;
   if (shape->T > 0 && (!logits || !topk_ids)) return MOE_ERR_ARG;
-  if (workspace_bytes < moe_balance_workspace_bytes(shape, sequences)) return MOE_ERR_ARG;
+  const int tiles = balance_tile_count(shape->T), stride = balance_stride(*shape);
+  if (workspace_bytes < balance_bytes(*shape, tiles, sequences)) return MOE_ERR_ARG;
   if (!aligned(logits, type_size(logits_type)) || !aligned(topk_ids, 4) ||
       !aligned(seq_offsets, 4) || !aligned(loss, 4) || !aligned(expert_counts, 4) ||
       !aligned(token_counts, 4) || !aligned(score_mean, 4) || !aligned(workspace, 16))
     return MOE_ERR_ARG;
-  const int tiles = balance_tile_count(shape->T), stride = balance_stride(*shape);
-  const size_t slots = balance_slots(*shape, sequences);
+  const size_t slots = size_t(tiles) + sequences;
   float* sums = static_cast<float*>(workspace);
   int32_t* pairs = reinterpret_cast<int32_t*>(sums + slots * stride);
   const BalanceArgs a{logits, topk_ids, seq_offsets, sums, pairs, pairs + slots * stride, loss,

@@ -547,7 +547,8 @@ int moe_balance_loss(const moe_shape_t* shape, const moe_router_t* router, int l
                      float* score_mean, void* workspace, size_t workspace_bytes,
                      int32_t* err_word, void* stream);
 
-/* Bytes of workspace of moe_balance_loss; 0 for an invalid shape or count. */
+/* Bytes of workspace of moe_balance_loss; 0 for an invalid shape or count. What
+ * it gives for a shape is enough for any fewer tokens, experts or sequences too. */
 size_t moe_balance_workspace_bytes(const moe_shape_t* shape, int sequences);
 
 #define MOE_ACT_NONE 0   /* out = y */

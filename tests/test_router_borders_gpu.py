@@ -230,3 +230,30 @@ def test_shares_of_far_logits(dtype, scoring, E):
         # as above, the quotients and sums over k, then the output's half step
         bound = (rel + (2 * k + 16) * ref.ULP) * size * (1 + step) + step * abs(want) + least + flushed
         assert (abs(got - want) <= bound).all()
+
+
+@pytest.mark.parametrize("most,T", [(2049, 2048), (2049, 33), (16385, 16384), (16385, 4097)])
+def test_balance_workspace_of_a_larger_batch(most, T):
+    """One workspace, made for the largest batch: smaller ones fit, and give what
+    they give in one of their own."""
+    E, k, S = 48, 4, 3
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    z = torch.randn(T, E, device="cuda", generator=g)
+    ids = torch.randint(0, E, (T, k), device="cuda", generator=g, dtype=torch.int32)
+    off = torch.tensor([0, T // 3, T // 2, T], dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = []
+    for size in (moe.balance_workspace_bytes(most, E, k, S), moe.balance_workspace_bytes(T, E, k, S)):
+        ws = torch.full((size + 64,), 0x5A, dtype=torch.uint8, device="cuda")
+        i32 = dict(dtype=torch.int32, device="cuda")
+        out = [torch.full((S,), -7.0, device="cuda"), torch.full((S, E), -7, **i32),
+               torch.full((S,), -7, **i32), torch.full((S, E), -7.0, device="cuda")]
+        moe.balance_loss(z, ids, moe.Router(), *out, workspace=ws[:size], seq_offsets=off, err=err)
+        torch.cuda.synchronize()
+        assert bool((ws[size:] == 0x5A).all()) and int(err.item()) == 0
+        got.append(out)
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    _, wc, wt, _ = ref.balance(z.double().cpu().numpy(), ids.cpu().numpy(), "softmax",
+                               off.cpu().numpy())
+    assert (got[0][1].cpu().numpy() == wc).all() and (got[0][2].cpu().numpy() == wt).all()
