@@ -763,9 +763,10 @@ def expert_product(fmt: str, rows: torch.Tensor, expert_counts, expert_offsets, 
     buffer times their experts' 4-bit weights into out [cap, N] bf16, or
     [cap, N / 2] with act "swiglu". fmt "mxfp4" or "nvfp4"; w_q [E, N, H / 2]
     and w_scale [E, N, H / 32 or H / 16] uint8; factor [E] float32 multiplies
-    an expert's products; T * k bounds the rows in use. expert_counts [E] and
-    expert_offsets [E + 1] are the layout's, or those of the experts [a, b) of
-    it with their weights: counts[a:b], offsets[a:b + 1]."""
+    an expert's products; the launch is laid out for T * k rows in use (other
+    numbers cost time, no rows). expert_counts [E] and expert_offsets [E + 1]
+    are the layout's, or those of the experts [a, b) of it with their weights:
+    counts[a:b], offsets[a:b + 1], and best a T of their share of the rows."""
     if fmt not in ("mxfp4", "nvfp4"):
         raise MoeError(f"unknown weight format {fmt!r}: mxfp4 or nvfp4")
     if act not in ACTS:

@@ -448,8 +448,9 @@ int moe_combine_ranks(const moe_shape_t* shape, const uint16_t* partial,
  *
  * Logits are [T, E], row-major without padding, of one of three types; the
  * arithmetic is in 32-bit floats or wider. -infinity masks an expert for a
- * token: it is never chosen and its score is 0. Only T, E, R and k of the
- * shape matter here.
+ * token: it is never chosen and its score is 0. Only T, E and k of the shape
+ * change anything here, but all of it has to keep the limits above (H = 8,
+ * R = 1, align = 1, block = 0 always do).
  */
 #define MOE_TYPE_F32 0
 #define MOE_TYPE_BF16 1
@@ -565,12 +566,16 @@ size_t moe_balance_workspace_bytes(const moe_shape_t* shape, int sequences);
  *   a row of W_e as a row of hidden states there: N rows of shape->H values,
  *   H/2 bytes of e2m1 codes (the even value in the low nibble), and one scale
  *   byte per 32 values (E8M0, MOE_WIRE_MXFP4) or per 16 (E4M3, MOE_WIRE_NVFP4).
- *   The products are summed in 32-bit floats, the weights' values exact, and
- *   rounded to bf16 once, after factor and activation.
- *   shape          T*k bounds the number of rows in use, H is their width (a multiple
- *                  of 32, at most 2^20), E the experts whose weights are given; to use the experts
- *                  [a, b) of a layout, pass E = b - a, expert_counts + a and
- *                  expert_offsets + a. R, align and block are not looked at.
+ *   The products are summed in 32-bit floats, the weights' values exact (one past
+ *   float32's range is infinite), and rounded to bf16 once, after factor and activation.
+ *   shape          T*k is the number of rows in use as far as the host knows it: the
+ *                  launch is laid out for that many (other numbers cost time, no rows).
+ *                  H is their width (a multiple of 32, at most 2^20), E the experts whose
+ *                  weights are given. To use the experts [a, b) of a layout, pass
+ *                  E = b - a, expert_counts + a and expert_offsets + a, and best a T of
+ *                  their share of the rows. R, align and block change nothing but have to
+ *                  keep the limits above: R = 1 (the layout's R need not divide b - a),
+ *                  align = 1 and block = 0 always do, whatever the layout's shape.
  *   N              rows of one expert's weights (1 <= N <= 2^24; even with MOE_ACT_SWIGLU, whose
  *                  gate is rows [0, N/2) and whose other factor rows [N/2, N))
  *   format         MOE_WIRE_MXFP4 or MOE_WIRE_NVFP4;  act  MOE_ACT_NONE or MOE_ACT_SWIGLU

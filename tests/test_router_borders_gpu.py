@@ -257,3 +257,30 @@ def test_balance_workspace_of_a_larger_batch(most, T):
     _, wc, wt, _ = ref.balance(z.double().cpu().numpy(), ids.cpu().numpy(), "softmax",
                                off.cpu().numpy())
     assert (got[0][1].cpu().numpy() == wc).all() and (got[0][2].cpu().numpy() == wt).all()
+
+
+@pytest.mark.parametrize("share", [150, 25, 4, 1])
+def test_product_of_a_slice_with_its_share_of_the_rows(share):
+    """The experts [a, b) of a layout with T * k the whole layout's rows, theirs,
+    or fewer: the same rows are written, each within its roundings."""
+    from test_experts_gpu import i32, layout, weights
+    rng = np.random.default_rng(31)
+    counts, H, N = [50, 9, 0, 12, 4, 75], 192, 40
+    off = layout(counts, 1, 0)
+    x = torch.from_numpy(rng.normal(size=(150, H)).astype(np.float32)).to(torch.bfloat16)
+    q, s = weights(rng, "mxfp4", 6, N, H)
+    out = torch.full((150, N), -77.0, dtype=torch.bfloat16, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    moe.expert_product("mxfp4", x.cuda(), i32(counts)[1:5], i32(off)[1:6], share, 1,
+                       torch.from_numpy(q[1:5]).cuda(), torch.from_numpy(s[1:5]).cuda(), out, err=err)
+    torch.cuda.synchronize()
+    got = out.double().cpu().numpy()
+    assert int(err.item()) == 0
+    assert (got[:50] == -77).all() and (got[75:] == -77).all()
+    for e in range(1, 5):
+        at = slice(int(off[e]), int(off[e + 1]))
+        w, xd = ref.weight_values("mxfp4", q[e], s[e]), x[at].double().numpy()
+        want, size = xd @ w.T, abs(xd) @ abs(w.T)
+        # counted as in test_experts_gpu.py
+        bound = (H / 32 * 8 + 8) * ref.ULP * size + 2.0 ** -8 * abs(want)
+        assert (abs(got[at] - want) <= bound).all()

@@ -52,3 +52,28 @@ def balance(T, E, S, workspace_bytes):
 def test_balance_refuses_a_short_workspace(T):
     for S in (1, 7):
         assert balance(T, 64, S, need(T, 64, S) - 1) == moe.MOE_ERR_ARG
+
+
+def test_shape_of_a_slice_of_the_experts():
+    """The products of a slice take a shape of their own: R = 1, whatever the
+    layout's R (8 experts of a rank of 32, say), align = 1 and block = 0. Fields
+    that change nothing have to keep the limits all the same."""
+    def product(**kw):
+        s = dict(T=0, H=512, E=8, R=1, k=8, align=1, block=0)
+        s.update(kw)
+        return moe.lib().moe_expert_product(moe.MoeShape(**s), 64, 2, 0, FAKE, FAKE, FAKE, 64,
+                                            FAKE, FAKE, None, FAKE, None, None)
+
+    def route(**kw):
+        s = dict(T=0, H=8, E=8, R=1, k=8, align=1, block=0)
+        s.update(kw)
+        return moe.lib().moe_route(moe.MoeShape(**s), ctypes.byref(moe.Router()), 0, FAKE, None,
+                                   None, FAKE, FAKE, None, None)
+
+    for call in (product, route):
+        assert call() == moe.MOE_OK  # no tokens: every check passed, nothing launched
+        assert call(E=256, R=32) == moe.MOE_OK and call(E=7) == moe.MOE_OK
+        for bad in (dict(R=32), dict(R=0), dict(align=0), dict(align=2, block=2), dict(block=-1),
+                    dict(H=12)):
+            assert call(**bad) == moe.MOE_ERR_ARG, bad
+    assert route(H=24) == moe.MOE_OK and product(H=24) == moe.MOE_ERR_ARG
