@@ -23,8 +23,8 @@
 // Measured (kernel time; E = 48): one token's 6 experts, H = 5120, N = 4096,
 // SwiGLU, MXFP4 (67 MB) 15 us; 64 tokens in NVFP4 (566 MB) 127 us, 4.5 TB/s; H =
 // 2048, N = 5120 in MXFP4 (267 MB) 63 us, 4.2 TB/s; 256 tokens top-8 of E = 32, H =
-// 7168, N = 4096 in MXFP4 (499 MB, 64 rows an expert) 179 us, up to 198 us in long
-// runs, where the clock falls. A kernel that only reads the codes in this
+// 7168, N = 4096 in MXFP4 (499 MB, 64 rows an expert) 185 us, 203 as the median of 15
+// calls and 242 of 30, where the clock falls. A kernel that only reads the codes in this
 // pattern takes 86 us and 47 us at the second and third size (5.9 and 5.3 TB/s).
 
 #include "moe_common.h"
@@ -511,7 +511,14 @@ int column_tiles(int form, bool swiglu, int wide) {
 // Few workgroups with long rows split H over the waves instead of columns:
 // 16.3 against 18.6 us for one token's 6 experts there (192 workgroups), 27
 // against 30 us for two tokens', but 49.1 against 49.2 us for four (768), and
-// at H = 2048 14.8 against 14.3 us for one.
+// at H = 2048 14.8 against 14.3 us for one. 48 experts with N = 4096 and more fill
+// the chip in every form; fewer or narrower ones were not measured. A mean of 8
+// would be 5% faster with 32 rows in MXFP4 and is 8% slower with them in NVFP4:
+// one rule for both. The mean is of T * k rows over all E experts, so it is
+// right for a slice of a layout's experts where T is their share: 192 rows of 48 of
+// 384 experts take 98 us then (MXFP4, H = 5120), 146 us with the layout's T = 256.
+// (The form of 16 rows without an activation keeps 2 registers in scratch in MXFP4
+// and 4 in NVFP4, for three waves a SIMD.)
 int form_of(const moe_shape_t& sh, bool swiglu, int wide, int64_t pairs, int64_t active) {
   const int64_t mean = (pairs + active - 1) / active;
   if (mean > 20) return 3;

@@ -714,7 +714,9 @@ constexpr int kTileWaves = kTileThreads / kWave;
 // slot tile + sequence (increasing along the tokens, so no two pairs of them
 // share one) and start anew. Bound by latency: T = 16384, E = 256 with
 // sigmoids of bfloat16 logits (8.4 MB) takes 9.6 us (23.7 us with a wave per
-// token), T = 4096, E = 384 in float32 6.7 us.
+// token), T = 4096, E = 384 in float32 6.8 us. A lane's float sum has a token a
+// pass: one or two up to T = 16384, T / 8192 past that (16 lanes a token; 4 times
+// as many with 64); the waves' 8 sums are joined in floats, tiles in 64 bits.
 template <typename Tz, int LT, int V, bool kSigmoid, bool kFull>
 __global__ __launch_bounds__(kTileThreads) void balance_tiles(BalanceArgs a) {
   extern __shared__ float lds_all[];
@@ -1157,7 +1159,7 @@ void by_type_tokens(int type, int E, Args&&... args) {
 
 // Tiles of the balance loss: a multiple of 32 tokens (a workgroup's pass), at
 // most 256 of them; two passes where one would make more than 64 tiles, for the join
-// reads every tile of a sequence (T = 4096, E = 384: 64 tiles 6.7 + 5.9 us, 128 tiles
+// reads every tile of a sequence (T = 4096, E = 384: 64 tiles 6.8 + 5.6 us, 128 tiles
 // 5.8 + 7.8 us, 32 tiles 10.1 + 5.1 us), and more only past 16384 tokens.
 constexpr int kMaxTiles = 256;
 constexpr int kOnePassTiles = 64;
