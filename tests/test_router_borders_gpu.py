@@ -1,5 +1,6 @@
-"""Router calls whose values lie at the borders of float32: group scores whose
-keys are much larger than their sum."""
+"""Calls at borders: group scores whose keys are much larger than their sum,
+or sum to an infinity; shares of logits as far out as their type goes; one
+workspace for batches of all sizes; the products of a slice of the experts."""
 import numpy as np
 import pytest
 import torch
