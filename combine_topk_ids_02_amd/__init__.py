@@ -36,6 +36,7 @@ EXPORTS = ("moe_abi_version", "moe_status_string", "moe_dispatch_layout",
            "moe_dispatch_pack_nvfp4", "moe_permute_by_expert_nvfp4",
            "moe_dispatch", "moe_dispatch_quantised", "moe_route", "moe_route_backward",
            "moe_balance_loss", "moe_balance_workspace_bytes", "moe_expert_product",
+           "moe_norm", "moe_norm_backward", "moe_norm_workspace_bytes", "moe_quantise_rows",
            "moe_testing_set_layout_form",
            "moe_testing_set_layout_match",
            "moe_testing_set_dispatch_fused", "moe_testing_time_next_launch")
@@ -51,6 +52,8 @@ LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 ROW_TYPES = (torch.bfloat16, torch.int16, torch.uint16)  # of the expert products' rows
 SCORINGS = {"softmax": 0, "sigmoid": 1}
 ACTS = {None: 0, "none": 0, "swiglu": 1}
+NORM_TYPES = {torch.float32: 0, torch.bfloat16: 1}  # of a norm's stream and weight
+NORM_FORMATS = {None: 0, "int8": 4, "mxfp8": 1}
 
 
 class MoeShape(ctypes.Structure):
@@ -137,6 +140,15 @@ def lib():
     L.moe_expert_product.restype = ctypes.c_int
     L.moe_expert_product.argtypes = [shp, ctypes.c_int, ctypes.c_int, ctypes.c_int, vp, vp, vp,
                                      i64, vp, vp, vp, vp, vp, vp]
+    ci, sz = ctypes.c_int, ctypes.c_size_t
+    L.moe_norm.restype = ci
+    L.moe_norm.argtypes = [shp, ci, vp, vp, vp, ci, vp, ctypes.c_float, vp, ci, vp, vp, vp, vp]
+    L.moe_norm_backward.restype = ci
+    L.moe_norm_backward.argtypes = [shp, ci, vp, vp, vp, ci, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_norm_workspace_bytes.restype = sz
+    L.moe_norm_workspace_bytes.argtypes = [shp]
+    L.moe_quantise_rows.restype = ci
+    L.moe_quantise_rows.argtypes = [shp, vp, vp, i64, vp, vp, vp, vp]
     L.moe_testing_set_dispatch_fused.restype = ctypes.c_int
     L.moe_testing_set_dispatch_fused.argtypes = [ctypes.c_int]
     L.moe_testing_set_layout_form.restype = ctypes.c_int
@@ -790,6 +802,111 @@ def expert_product(fmt: str, rows: torch.Tensor, expert_counts, expert_offsets, 
           _dev(w_scale, "w_scale", u8, (E, N, H // WIRE_FORMATS[fmt][1]), dev),
           _dev(factor, "factor", torch.float32, (E,), dev),
           _dev(out, "out", out.dtype, (cap, N // 2 if code else N), dev), _dev_err(err, dev))
+
+
+def _norm_type(t: torch.Tensor, name: str) -> int:
+    code = NORM_TYPES.get(t.dtype)
+    if code is None:
+        raise MoeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    return code
+
+
+def norm(x: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6, residual=None, sum=None,
+         out=None, fmt: str | None = None, q=None, q_scale=None, inv_rms=None) -> None:
+    """moe_norm: the root-mean-square norm of x [T, H] bf16, or of x + residual,
+    times weight [H] (float32 or bfloat16). residual and sum [T, H] are float32 or
+    bfloat16, sum the rounded x + residual (it may be the residual itself). The
+    result goes to out [T, H] bf16, to codes, or to both: fmt "int8" with q
+    [T, H] int8 and q_scale [T] float32, or "mxfp8" with q [T, H] and q_scale
+    [T, H / 32] uint8. inv_rms [T] float32 is what norm_backward() needs."""
+    dev = x.device
+    if dev.type != "cuda":
+        raise MoeError("tensors must be on the GPU")
+    if fmt not in NORM_FORMATS:
+        raise MoeError(f"unknown format {fmt!r}: int8 or mxfp8")
+    if x.dim() != 2 or x.dtype not in ROW_TYPES:
+        raise MoeError(f"x must be [T, H] of bf16 (or its bits), got {tuple(x.shape)} of {x.dtype}")
+    if (residual is None) != (sum is None):
+        raise MoeError("give residual and sum, or neither")
+    if (fmt is None) != (q is None) or (fmt is None) != (q_scale is None):
+        raise MoeError("q and q_scale go with a format")
+    if out is None and q is None:
+        raise MoeError("give out, q or both")
+    T, H = x.shape
+    bf16, f32 = torch.bfloat16, torch.float32
+    stream = bf16 if residual is None else residual.dtype
+    code = 1 if residual is None else _norm_type(residual, "residual")
+    kind, scales = (torch.int8, (T,)) if fmt == "int8" else (torch.uint8, (T, H // 32))
+    _call(lib().moe_norm, "moe_norm", dev, _sizes(T, H, 1, 1), code,
+          _dev(x, "x", x.dtype, (T, H), dev), _dev(residual, "residual", stream, (T, H), dev),
+          _dev(sum, "sum", stream, (T, H), dev), _norm_type(weight, "weight"),
+          _dev(weight, "weight", weight.dtype, (H,), dev), eps,
+          _dev(out, "out", bf16 if out is None or out.dtype not in ROW_TYPES else out.dtype,
+               (T, H), dev), NORM_FORMATS[fmt], _dev(q, "q", kind, (T, H), dev),
+          _dev(q_scale, "q_scale", f32 if fmt == "int8" else kind, scales, dev),
+          _dev(inv_rms, "inv_rms", f32, (T,), dev))
+
+
+def norm_workspace_bytes(T: int, H: int) -> int:
+    """moe_norm_workspace_bytes: scratch that norm_backward() needs for the
+    weight's gradient, for this many tokens or fewer."""
+    return int(lib().moe_norm_workspace_bytes(_sizes(T, H, 1, 1)))
+
+
+def norm_backward(d_out: torch.Tensor, sum: torch.Tensor, inv_rms, weight, *, d_sum=None,
+                  d_x=None, d_residual=None, d_weight=None, workspace=None) -> None:
+    """moe_norm_backward: from d_out [T, H] bf16 (the gradient of norm()'s
+    result), sum and inv_rms as norm() wrote them (sum: x where there was no
+    residual) and d_sum [T, H] (the gradient that reaches the sum from elsewhere,
+    of the sum's type), the gradient of x and the residual into d_x [T, H] bf16
+    and d_residual [T, H] of the sum's type, and the weight's into d_weight [H]
+    float32 (with workspace: a device tensor of norm_workspace_bytes bytes)."""
+    dev = d_out.device
+    if dev.type != "cuda":
+        raise MoeError("tensors must be on the GPU")
+    if d_out.dim() != 2 or d_out.dtype not in ROW_TYPES:
+        raise MoeError("d_out must be [T, H] of bf16 (or its bits), got "
+                       f"{tuple(d_out.shape)} of {d_out.dtype}")
+    if d_x is None and d_residual is None and d_weight is None:
+        raise MoeError("give d_x, d_residual or d_weight")
+    if d_weight is not None and workspace is None:
+        raise MoeError("d_weight needs a workspace of norm_workspace_bytes bytes")
+    T, H = d_out.shape
+    code, stream, f32 = _norm_type(sum, "sum"), sum.dtype, torch.float32
+    room = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call(lib().moe_norm_backward, "moe_norm_backward", dev, _sizes(T, H, 1, 1), code,
+          _dev(d_out, "d_out", d_out.dtype, (T, H), dev), _dev(sum, "sum", stream, (T, H), dev),
+          _dev(inv_rms, "inv_rms", f32, (T,), dev), _norm_type(weight, "weight"),
+          _dev(weight, "weight", weight.dtype, (H,), dev),
+          _dev(d_sum, "d_sum", stream, (T, H), dev),
+          _dev(d_x, "d_x", torch.bfloat16 if d_x is None or d_x.dtype not in ROW_TYPES
+               else d_x.dtype, (T, H), dev),
+          _dev(d_residual, "d_residual", stream, (T, H), dev),
+          _dev(d_weight, "d_weight", f32, (H,), dev),
+          None if workspace is None else _dev(workspace, "workspace", workspace.dtype,
+                                              workspace.shape, dev), room)
+
+
+def quantise_rows(rows: torch.Tensor, q, scale, *, pair_row=None, err=None) -> None:
+    """moe_quantise_rows: rows [cap, H] bf16 to q [cap, H] int8 with scale [cap]
+    float32: the rows that pair_row [T, k] (the layout's) names, or all of them."""
+    dev = rows.device
+    if dev.type != "cuda":
+        raise MoeError("tensors must be on the GPU")
+    if rows.dim() != 2 or rows.dtype not in ROW_TYPES:
+        raise MoeError(f"rows must be [cap, H] of bf16 (or its bits), got {tuple(rows.shape)} of "
+                       f"{rows.dtype}")
+    cap, H = rows.shape
+    T, k = cap, 1
+    if pair_row is not None:
+        if pair_row.dim() != 2:
+            raise MoeError(f"pair_row has shape {tuple(pair_row.shape)}, the call needs [T, k]")
+        T, k = pair_row.shape
+    _call(lib().moe_quantise_rows, "moe_quantise_rows", dev, _sizes(T, H, k, k),
+          _dev(rows, "rows", rows.dtype, (cap, H), dev),
+          _dev(pair_row, "pair_row", torch.int32, (T, k), dev), cap,
+          _dev(q, "q", torch.int8, (cap, H), dev),
+          _dev(scale, "scale", torch.float32, (cap,), dev), _dev_err(err, dev))
 
 
 def time_next_launch(start: "torch.cuda.Event | None", stop: "torch.cuda.Event | None") -> None:

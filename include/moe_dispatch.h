@@ -599,6 +599,95 @@ int moe_expert_product(const moe_shape_t* shape, int N, int format, int act,
                        int32_t* err_word, void* stream);
 
 /*
+ * The norm before a layer, its gradient, and rows to 8-bit integers
+ *
+ * Of the shape T and H change anything in the norm's calls, T, H and k in
+ * moe_quantise_rows; all of it has to keep the limits above (E = 1, R = 1, k = 1,
+ * align = 1, block = 0 always do). H <= 32,768 (65,536 for moe_quantise_rows).
+ *
+ * Rows in 8-bit integers, beside the wire formats: a row of H values v is H
+ * bytes, codes q in [-127, 127], and one float32 scale s = max|v| / 127, so that
+ * v is about q * s; q is the whole number nearest to v * (127 / max|v|), ties to
+ * even, in float32. A row of zeros has scale 0; one that holds a NaN or an
+ * infinity has a NaN scale and codes 0.
+ */
+#define MOE_ROWS_INT8 4
+
+/*
+ * Root-mean-square norm with the residual's addition ([GPUs] sec 5: the sum of
+ * a layer's output and the residual stream is normalised for the next layer, and
+ * its rows may be quantised in the same pass):
+ *   sum = x + residual, rounded to the stream's type (x where there is none)
+ *   inv_rms[t] = 1 / sqrt(mean over the row of sum^2 + eps)
+ *   y = sum * inv_rms * weight
+ * The norm is of the rounded sum, which is what the next layer and the gradient
+ * read. Everything is in float32 (a row whose squares pass its range, magnitudes
+ * from about 2^63, gets inv_rms 0); y is rounded once, to bf16 and from 32 bits to the
+ * codes.
+ *   stream_type  MOE_TYPE_BF16 or MOE_TYPE_F32: of residual and sum
+ *   x            [T*H] in: bf16
+ *   residual     [T*H] in: or NULL, then sum is NULL too
+ *   sum          [T*H] out: may be the residual's own buffer, or x's (bf16)
+ *   weight_type, weight  MOE_TYPE_BF16 or MOE_TYPE_F32, [H] in
+ *   eps          > 0, finite
+ *   out          [T*H] out: y in bf16, or NULL; may be x's buffer, or with a bf16
+ *                stream the residual's where sum is not
+ *   format       0: no codes; MOE_ROWS_INT8: q [T*H] int8, q_scale [T] float32;
+ *                MOE_WIRE_MXFP8: q [T*H] and q_scale [T*H/32] bytes as
+ *                moe_dispatch_pack_mxfp8 makes them, of y in 32 bits (H % 32 == 0)
+ *   q, q_scale   out: NULL with format 0. out or q has to be given.
+ *   inv_rms      [T] out: float32, or NULL
+ * Buffers that are not one and the same must not overlap. All are 16-byte aligned,
+ * q_scale and inv_rms 4-byte. One launch.
+ */
+int moe_norm(const moe_shape_t* shape, int stream_type, const uint16_t* x, const void* residual,
+             void* sum, int weight_type, const void* weight, float eps, uint16_t* out, int format,
+             void* q, void* q_scale, float* inv_rms, void* stream);
+
+/*
+ * The gradient of moe_norm's y and sum (the codes have none): with
+ * g = d_out * weight and u = sum * inv_rms,
+ *   d = inv_rms * (g - u * mean over the row of g * u) + d_sum
+ * is the gradient of x and of the residual alike, and
+ *   d_weight[c] = sum over the rows of d_out * u.
+ *   d_out       [T*H] in: bf16, the gradient of y
+ *   sum, inv_rms  in: as moe_norm wrote them (sum: x where there was no residual)
+ *   d_sum       [T*H] in: the gradient that reaches the sum from elsewhere, of the
+ *               stream's type, or NULL
+ *   d_x         [T*H] out: d in bf16, or NULL; may be d_out's buffer
+ *   d_residual  [T*H] out: d in the stream's type, or NULL; may be d_sum's buffer. (With
+ *               a bf16 stream d_x and d_residual are the same values.)
+ *   d_weight    [H] out: float32, or NULL; 0 for T = 0
+ *   workspace   [workspace_bytes] scratch of moe_norm_workspace_bytes bytes or more,
+ *               16-byte aligned, as for moe_dispatch_layout (no clearing needed; not
+ *               shared by calls that run at the same time). Needed only with d_weight.
+ * At least one of d_x, d_residual and d_weight has to be given. The sums do not
+ * depend on timing. One launch, two with d_weight.
+ */
+int moe_norm_backward(const moe_shape_t* shape, int stream_type, const uint16_t* d_out,
+                      const void* sum, const float* inv_rms, int weight_type, const void* weight,
+                      const void* d_sum, uint16_t* d_x, void* d_residual, float* d_weight,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of moe_norm_backward (at most 512 * H * 4); 0 for an invalid
+ * shape. What it gives for a shape is enough for any fewer tokens too. */
+size_t moe_norm_workspace_bytes(const moe_shape_t* shape);
+
+/*
+ * Rows to 8-bit integers, as above: the rows of the expert-grouped buffer that
+ * hold a pair, or all rows.
+ *   rows       [cap_expert*H] in: bf16
+ *   pair_row   [T*k] in: from the layout: only the rows it names are read and written
+ *              (-1 is skipped; rows at or past cap_expert are skipped and flagged,
+ *              MOE_ERRBIT_EXPERT_CAP); or NULL: rows [0, T*k), at most cap_expert
+ *   q          [cap_expert*H] out, scale [cap_expert] out
+ * rows and q 16-byte aligned. One launch.
+ */
+int moe_quantise_rows(const moe_shape_t* shape, const uint16_t* rows, const int32_t* pair_row,
+                      int64_t cap_expert, int8_t* q, float* scale, int32_t* err_word,
+                      void* stream);
+
+/*
  * Testing hook (not for production callers; it changes a process-wide setting
  * of this library and returns the previous value): which form of the layout
  * runs when a workspace is given: -1 (default) by size as described at
@@ -627,7 +716,7 @@ int moe_testing_set_dispatch_fused(int fused);
 /*
  * Measurement hook (not for production callers; process-wide, not
  * thread-safe): the next kernel the dispatch and combine calls launch (the
- * router, balance and expert calls leave it armed), on any stream, has the
+ * router, balance, norm and expert calls leave it armed), on any stream, has the
  * runtime record start_event as it begins and stop_event as it ends, so that
  * hipEventElapsedTime(start_event, stop_event) is that kernel's own duration.
  * The events are the caller's (hipEvent_t as void*, created with timing
