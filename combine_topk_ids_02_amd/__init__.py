@@ -37,6 +37,7 @@ EXPORTS = ("moe_abi_version", "moe_status_string", "moe_dispatch_layout",
            "moe_dispatch", "moe_dispatch_quantised", "moe_route", "moe_route_backward",
            "moe_balance_loss", "moe_balance_workspace_bytes", "moe_expert_product",
            "moe_norm", "moe_norm_backward", "moe_norm_workspace_bytes", "moe_quantise_rows",
+           "moe_int8_product",
            "moe_testing_set_layout_form",
            "moe_testing_set_layout_match",
            "moe_testing_set_dispatch_fused", "moe_testing_time_next_launch")
@@ -149,6 +150,8 @@ def lib():
     L.moe_norm_workspace_bytes.argtypes = [shp]
     L.moe_quantise_rows.restype = ci
     L.moe_quantise_rows.argtypes = [shp, vp, vp, i64, vp, vp, vp, vp]
+    L.moe_int8_product.restype = ci
+    L.moe_int8_product.argtypes = [shp, ci, ci, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp]
     L.moe_testing_set_dispatch_fused.restype = ctypes.c_int
     L.moe_testing_set_dispatch_fused.argtypes = [ctypes.c_int]
     L.moe_testing_set_layout_form.restype = ctypes.c_int
@@ -907,6 +910,41 @@ def quantise_rows(rows: torch.Tensor, q, scale, *, pair_row=None, err=None) -> N
           _dev(pair_row, "pair_row", torch.int32, (T, k), dev), cap,
           _dev(q, "q", torch.int8, (cap, H), dev),
           _dev(scale, "scale", torch.float32, (cap,), dev), _dev_err(err, dev))
+
+
+def int8_product(rows: torch.Tensor, row_scale, w_q, w_scale, out, *, act: str | None = None,
+                 expert_counts=None, expert_offsets=None, T: int | None = None, k: int = 1,
+                 err=None) -> None:
+    """moe_int8_product: rows [cap, H] int8 with row_scale [cap] float32 times
+    weights w_q [E, N, H] int8 with w_scale [E, N] float32 into out [cap, N] bf16,
+    or [cap, N / 2] with act "swiglu". With expert_counts [E] and expert_offsets
+    [E + 1] (the layout's, or those of a slice of its experts, as for
+    expert_product()) the rows are the expert-grouped buffer's, and T * k of them
+    are in use as far as the host knows; without, all rows (or the first T * k)
+    have the one expert."""
+    if act not in ACTS:
+        raise MoeError(f"unknown activation {act!r}: one of {sorted(a for a in ACTS if a)}")
+    dev = rows.device
+    if dev.type != "cuda":
+        raise MoeError("tensors must be on the GPU")
+    if rows.dim() != 2 or w_q.dim() != 3:
+        raise MoeError("rows must be [cap, H] and w_q [E, N, H]")
+    if (expert_counts is None) != (expert_offsets is None):
+        raise MoeError("give expert_counts and expert_offsets, or neither")
+    cap, H = rows.shape
+    E, N, _ = w_q.shape
+    code = ACTS[act]
+    i8, i32, f32 = torch.int8, torch.int32, torch.float32
+    if T is None:
+        T = cap // k
+    if out.dtype not in ROW_TYPES:
+        raise MoeError(f"out must be bf16 (or its bits), got {out.dtype}")
+    _call(lib().moe_int8_product, "moe_int8_product", dev, _sizes(T, H, E, k), N, code,
+          _dev(rows, "rows", i8, (cap, H), dev), _dev(row_scale, "row_scale", f32, (cap,), dev),
+          _dev(expert_counts, "expert_counts", i32, (E,), dev),
+          _dev(expert_offsets, "expert_offsets", i32, (E + 1,), dev), cap,
+          _dev(w_q, "w_q", i8, (E, N, H), dev), _dev(w_scale, "w_scale", f32, (E, N), dev),
+          _dev(out, "out", out.dtype, (cap, N // 2 if code else N), dev), _dev_err(err, dev))
 
 
 def time_next_launch(start: "torch.cuda.Event | None", stop: "torch.cuda.Event | None") -> None:

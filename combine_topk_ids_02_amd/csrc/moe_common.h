@@ -1,4 +1,4 @@
-// What the router's and the expert products' kernels share: the wave's
+// What the router's, the norm's and the products' kernels share: the wave's
 // helpers, the limits of a shape and the host's checks.
 #pragma once
 
@@ -85,6 +85,37 @@ __device__ __forceinline__ float wave_sum(float v) {
   v += dpp<kRowBcast15, 0xA>(0.0f, v);
   v += dpp<kRowBcast31, 0xC>(0.0f, v);
   return read_lane(v, 63);
+}
+
+// The first row of expert e in the buffer and how many are in use, without the
+// rows that the buffer does not hold (`over`: there are such).
+__device__ __forceinline__ int run_of(const int32_t* counts, const int32_t* offsets, int64_t cap,
+                                      int e, int64_t* first, bool* over) {
+  const int64_t begin = offsets[e], end = offsets[e + 1];
+  const int64_t n = min((int64_t)counts[e], end - begin), held = min(n, cap - begin);
+  *first = begin;
+  *over = (begin >= 0) & (held < n) & (n > 0);
+  return ((begin < 0) | (held <= 0)) ? 0 : int(held);
+}
+
+typedef __amdgpu_buffer_rsrc_t buffer;
+
+// A buffer of `bytes` from p; a load past its end gives 0 and touches nothing.
+// (The same for the whole wave; the reads of the first lane say so.)
+__device__ __forceinline__ buffer make_buffer(const void* p, int bytes) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(uint32_t(v >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(uint64_t(hi) << 32 | lo), 0,
+                                           __builtin_amdgcn_readfirstlane(bytes), 0x00027000);
+}
+
+// `off` where `in`, else past the end (opaque: the compiler would make two
+// loads and a branch of it).
+__device__ __forceinline__ int offset_if(bool in, int off) {
+  int r = in ? off : 0x7FFFFF00;
+  asm("" : "+v"(r));
+  return r;
 }
 
 // The limits of moe_dispatch.h's "Common conventions" that concern T, H, E, R,

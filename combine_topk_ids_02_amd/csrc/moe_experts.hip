@@ -91,14 +91,8 @@ __device__ __forceinline__ bf16x8 expand_e4m3(uint32_t w, float scale) {
   return r;
 }
 
-// The first row of expert e in the buffer and how many are in use, without the
-// rows that the buffer does not hold (`over`: there are such).
 __device__ __forceinline__ int run_of(const ProductArgs& a, int e, int64_t* first, bool* over) {
-  const int64_t begin = a.offsets[e], end = a.offsets[e + 1];
-  const int64_t n = min((int64_t)a.counts[e], end - begin), held = min(n, a.cap - begin);
-  *first = begin;
-  *over = (begin >= 0) & (held < n) & (n > 0);
-  return ((begin < 0) | (held <= 0)) ? 0 : int(held);
+  return moe::run_of(a.counts, a.offsets, a.cap, e, first, over);
 }
 
 // Chunks of an expert; one (without rows) where the buffer holds none of its
@@ -144,26 +138,6 @@ __device__ __forceinline__ bool chunk_of(const ProductArgs& a, bool beyond, int 
     at -= total;
   }
   return false;
-}
-
-typedef __amdgpu_buffer_rsrc_t buffer;
-
-// A buffer of `bytes` from p; a load past its end gives 0 and touches nothing.
-// (The same for the whole wave; the reads of the first lane say so.)
-__device__ __forceinline__ buffer make_buffer(const void* p, int bytes) {
-  const uint64_t v = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(v));
-  const uint32_t hi = __builtin_amdgcn_readfirstlane(uint32_t(v >> 32));
-  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(uint64_t(hi) << 32 | lo), 0,
-                                           __builtin_amdgcn_readfirstlane(bytes), 0x00027000);
-}
-
-// `off` where `in`, else past the end (opaque: the compiler would make two
-// loads and a branch of it).
-__device__ __forceinline__ int offset_if(bool in, int off) {
-  int r = in ? off : 0x7FFFFF00;
-  asm("" : "+v"(r));
-  return r;
 }
 
 // What a wave takes of one granule of H (256 values) from the codes: two loads

@@ -688,6 +688,32 @@ int moe_quantise_rows(const moe_shape_t* shape, const uint16_t* rows, const int3
                       void* stream);
 
 /*
+ * Products in 8-bit integers: the rows of the expert-grouped buffer, or plain
+ * rows (a shared expert's), times weights, both as rows of 8-bit integers with a
+ * float32 scale each (MOE_ROWS_INT8; any code of int8 is taken):
+ *   y[r][n] = row_scale[r] * w_scale[e][n] * sum over H of rows[r][h] * w_q[e][n][h]
+ * The sums are exact (int32); the scales and the activation are applied in float32
+ * and the result is rounded to bf16 once. Any number of rows, from one to a
+ * prefill's.
+ *   shape          as for moe_expert_product: T*k rows in use as far as the host knows (the
+ *                  launch is laid out for that many), H their width (a multiple of
+ *                  16, at most 65,536), E the experts whose weights are given
+ *   N, act         as for moe_expert_product (N <= 2^24)
+ *   rows           [cap_expert*H] in: int8;  row_scale [cap_expert] in: float32
+ *   expert_counts [E], expert_offsets [E+1]  in: as for moe_expert_product; or both
+ *                  NULL: the T*k rows from the first on (at most cap_expert) all have
+ *                  the one expert (E = 1)
+ *   w_q            [E*N*H] in: int8;  w_scale [E*N] in: float32
+ *   out            [cap_expert*N], or [cap_expert*N/2] with MOE_ACT_SWIGLU, out: bf16;
+ *                  only the rows in use are written. Must not overlap the inputs.
+ * rows, w_q and out 16-byte aligned. One launch.
+ */
+int moe_int8_product(const moe_shape_t* shape, int N, int act, const int8_t* rows,
+                     const float* row_scale, const int32_t* expert_counts,
+                     const int32_t* expert_offsets, int64_t cap_expert, const int8_t* w_q,
+                     const float* w_scale, uint16_t* out, int32_t* err_word, void* stream);
+
+/*
  * Testing hook (not for production callers; it changes a process-wide setting
  * of this library and returns the previous value): which form of the layout
  * runs when a workspace is given: -1 (default) by size as described at
