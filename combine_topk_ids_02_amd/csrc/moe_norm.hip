@@ -121,27 +121,28 @@ __device__ __forceinline__ uint32_t join_max(uint32_t v, uint32_t* at, int wave,
   return total;
 }
 
-// A row's values in 127ths of the largest magnitude `top` (its bits). The
-// scale is top / 127 and the factor 127 / top, each rounded once; a code is the
-// nearest whole number to the float32 product v * factor, so that only a
-// quotient next to the middle between two codes may go to either. Tops whose
-// factor would leave float32's range are raised by 2^64 first, with the values.
+// A row's values in 127ths of the largest magnitude `top` (its bits). The scale
+// is top / 127 and the factor 127 * (1 / top), rounded at each step; a code is the
+// nearest whole number to the float32 product v * factor, so that only a quotient
+// next to the middle between two codes may go to either. Tops whose reciprocal
+// would come near the ends of float32's range are moved by 2^64 first, with the
+// values.
 struct Int8Scale {
   float scale, factor;  // factor 0: all codes are 0 (a row of zeros, or not finite)
-  bool tiny;
+  float move;
   __device__ __forceinline__ explicit Int8Scale(uint32_t top) {
     const float t = __uint_as_float(top);
     const bool finite = top < 0x7F800000u;
-    tiny = t < 0x1p-64f;
+    move = t < 0x1p-64f ? 0x1p64f : t > 0x1p64f ? 0x1p-64f : 1.0f;
     scale = finite ? t / 127.0f : __uint_as_float(0x7FC00000u);
-    factor = finite && top > 0 ? 127.0f / (tiny ? t * 0x1p64f : t) : 0.0f;
+    factor = finite && top > 0 ? 127.0f * (1.0f / (t * move)) : 0.0f;
   }
   __device__ __forceinline__ vec2 codes(Row8 r) const {
     vec2 q = {0, 0};
-    if (factor == 0.0f) return q;  // uniform, as `tiny` is
-    if (tiny) {
+    if (factor == 0.0f) return q;  // uniform, as `move` is
+    if (move != 1.0f) {
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) r.v[i] *= 0x1p64f;
+      for (int i = 0; i < kPiece; ++i) r.v[i] *= move;
     }
 #pragma unroll
     for (int i = 0; i < kPiece; ++i)

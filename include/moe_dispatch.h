@@ -607,9 +607,9 @@ int moe_expert_product(const moe_shape_t* shape, int N, int format, int act,
  *
  * Rows in 8-bit integers, beside the wire formats: a row of H values v is H
  * bytes, codes q in [-127, 127], and one float32 scale s = max|v| / 127, so that
- * v is about q * s; q is the whole number nearest to v * (127 / max|v|), ties to
- * even, in float32. A row of zeros has scale 0; one that holds a NaN or an
- * infinity has a NaN scale and codes 0.
+ * v is about q * s; q is the whole number nearest to v * (127 * (1 / max|v|)), ties
+ * to even, each step in float32. A row of zeros has scale 0; one that holds a NaN or
+ * an infinity has a NaN scale and codes 0.
  */
 #define MOE_ROWS_INT8 4
 

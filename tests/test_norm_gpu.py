@@ -346,7 +346,7 @@ def test_quantise_rows(H):
         rows = (randn(g, T, H) * torch.exp(3 * randn(g, T, 1))).to(torch.bfloat16)
         q, s, err = quantise(rows)
         assert err == 0
-        check_int8(q, s, rows.to(F64), 2 * ULP, 2 * ULP)  # the factor and the product
+        check_int8(q, s, rows.to(F64), 2 * ULP, 2 * ULP)  # reciprocal, factor, product
 
 
 def test_quantise_rows_of_every_size():
