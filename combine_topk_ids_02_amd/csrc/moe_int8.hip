@@ -3,13 +3,17 @@
 //
 // out = rows times weights, both int8 with K values a row, summed exactly in
 // int32 (K < 2^17), then scaled and activated in float32. Because the sums are
-// exact, H may be cut and joined in any order. Two kernels:
-//  - product_few, for few rows: the weights' bytes are the time. A workgroup takes
-//    at most 64 rows and 32 weight rows, each wave a part of K: both
-//    operands go straight into MFMA registers, whole cache lines of each row,
-//    several granules ahead, and the waves' sums meet in LDS;
-//  - product_tile, for many: tiles of both come to LDS without passing through
-//    registers while the tile before is multiplied.
+// exact, K may be cut and joined in any order.
+//
+// Two kernels, which bring 128 bytes of each of their rows and weight rows at a time to
+// LDS by loads that pass through no register, several such steps ahead:
+//  - product_few, for few rows, cuts K over the waves of a workgroup, so that few
+//    weight rows make many workgroups; their sums meet in LDS at the end. No wave
+//    waits for another before that;
+//  - product_tile, for many, has the waves share a tile of 64 to 256 rows.
+// (Straight into MFMA's registers, 16 rows' 64 bytes an instruction, one token's
+// product with K = 5,120, N = 4,096 took 9.4 us instead of 6.5, and 384 rows of 48 experts
+// 317 us instead of 171, which is 5.9 TB/s of the weights.)
 
 #include "moe_common.h"
 
@@ -17,6 +21,8 @@ namespace {
 
 using namespace moe;
 
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
@@ -122,21 +128,36 @@ __device__ __forceinline__ void place_of(int64_t i, int total, int tiles, int* c
   *col = int(rest / held);
 }
 
+// 16 bytes a lane from a buffer to LDS, lane l's to at + 16 l (`at` the same for
+// the whole wave), without a register in between; counted as a vector load.
+__device__ __forceinline__ void load_to_lds(const buffer& b, char* at, int off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      b, (__attribute__((address_space(3))) void*)at, 16, off, 0, 0, 0);
+}
+
 __device__ __forceinline__ float swiglu(float gate, float up) {
   return gate / (1.0f + expf(-gate)) * up;
 }
 
 // ---------------------------------------------------------------------------
 
-// W waves, each a part of K, of 16 * MT rows and 16 * NT weight rows.
-template <bool kSwiglu, int MT, int NT, int W, int D>
+// W waves, each a part of K, of 16 * MT rows and 16 * NT weight rows. A wave has
+// S granules in its own part of LDS, S - 1 of them on their way.
+template <bool kSwiglu, int MT, int NT, int W, int S>
 __global__ __launch_bounds__(W * kWave) void product_few(Int8Args a) {
-  static_assert(!kSwiglu || NT == 2, "a tile of gates and one of the other factors");
+  static_assert(NT <= 2, "with SwiGLU half a tile, or a tile, of gates and of the other factors");
+  static_assert(S >= 2 && S <= 4, "waits are written for these");
+  constexpr bool kMixed = kSwiglu && NT == 1;  // 8 gates and the 8 factors that they meet
   constexpr int BM = 16 * MT;
-  constexpr int kCols = 16 * (kSwiglu ? NT / 2 : NT);
-  __shared__ int part[W][NT * MT * 4][kWave];
+  constexpr int kCols = kSwiglu ? 8 * NT : 16 * NT;
+  constexpr int L = 2 * (NT + MT);         // loads of a granule, 8 rows each
+  constexpr int kStage = L * 8 * kGranule;
+  constexpr int kJoin = W * NT * MT * 4 * kWave * 4;
+  __shared__ __align__(16) char lds[W * S * kStage > kJoin ? W * S * kStage : kJoin];
+  int(*part)[NT * MT * 4][kWave] = reinterpret_cast<int(*)[NT * MT * 4][kWave]>(lds);
   const int lane = lane_id(), wave = wave_in_block();
   const int m = lane & 15, kq = lane >> 4;
+  char* mine = lds + wave * S * kStage;
   const int half = a.N / 2, limit = kSwiglu ? half : a.N;
   const int granules = (a.K + kGranule - 1) / kGranule;
   const int each = (granules + W - 1) / W;
@@ -149,32 +170,34 @@ __global__ __launch_bounds__(W * kWave) void product_few(Int8Args a) {
     place_of(i, chunks.total, a.tiles, &chunk, &col);
     if (!chunks.get(chunk, &e, &row0, &nr)) return;
     const int n0 = col * kCols;
+    const int8_t* w0 = a.w + (int64_t(e) * a.N + n0) * a.K;
     buffer wb[NT];
 #pragma unroll
     for (int h = 0; h < NT; ++h) {
-      const int n = kSwiglu ? n0 : n0 + 16 * h;
-      wb[h] = make_buffer(a.w + (int64_t(e) * a.N + n + (kSwiglu ? h * half : 0)) * a.K,
-                          max(0, min(16, limit - n)) * a.K);
+      if (kMixed)
+        wb[h] = make_buffer(w0, (half + min(8, limit - n0)) * a.K);
+      else
+        wb[h] = make_buffer(w0 + int64_t(kSwiglu ? h * half : 16 * h) * a.K,
+                            max(0, min(16, limit - (kSwiglu ? n0 : n0 + 16 * h))) * a.K);
     }
     const buffer xb = make_buffer(a.rows + row0 * a.K, nr * a.K);
-    i32x4 w[D][2][NT], x[D][2][MT];
-    auto load = [&](int d, int s) {
-      __builtin_amdgcn_sched_barrier(0);
+
+    // Load j fills rows 8 j .. 8 j + 7 of a granule: the weights' tiles, then the
+    // rows'; a lane 16 bytes, lane l the slot l % 8 of row l / 8. Slot s of row r
+    // holds piece s ^ (r / 2) % 8: 16 rows' same piece lies in different banks.
+    int from[L];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int k = (g0 + s) * kGranule + (4 * u + kq) * 16;
-        const int off = offset_if(s < steps && k < a.K, m * a.K + k);
+    for (int j = 0; j < L; ++j) {
+      const int r = 8 * j + (lane >> 3), piece = (lane & 7) ^ (r / 2 & 7);
+      const int row = j >= 2 * NT ? r - 16 * NT : kMixed && j == 1 ? r - 8 + half : r % 16;
+      from[j] = row * a.K + g0 * kGranule + piece * 16;
+    }
+    auto load = [&](int s, int slot) {
 #pragma unroll
-        for (int h = 0; h < NT; ++h)
-          w[d][u][h] =
-              __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(wb[h], off, 0, 0));
-#pragma unroll
-        for (int q = 0; q < MT; ++q)
-          x[d][u][q] = __builtin_bit_cast(
-              i32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                         xb, off == 0x7FFFFF00 ? off : off + q * 16 * a.K, 0, 0));
+      for (int j = 0; j < L; ++j) {
+        const buffer& b = j < 2 * NT ? wb[j / 2 % NT] : xb;
+        load_to_lds(b, mine + slot * kStage + j * 8 * kGranule, from[j] + s * kGranule);
       }
-      __builtin_amdgcn_sched_barrier(0);
     };
     i32x4 acc[NT][MT];
 #pragma unroll
@@ -182,21 +205,50 @@ __global__ __launch_bounds__(W * kWave) void product_few(Int8Args a) {
 #pragma unroll
       for (int q = 0; q < MT; ++q) acc[h][q] = i32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int d = 0; d < D; ++d) load(d, d);
-    for (int s0 = 0; s0 < steps; s0 += D) {
+    for (int s = 0; s < S - 1; ++s)
+      if (s < steps) load(s, s);
+    int slot = 0;
+    for (int s = 0; s < steps; ++s) {
+      // this granule has come when at most the later ones are on their way, and
+      // the reads of the slot that is filled next are done
+      const int later = min(S - 2, steps - 1 - s);
+      if (S > 3 && later == 2)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(2 * L) : "memory");
+      else if (S > 2 && later == 1)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(L) : "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      if (s + S - 1 < steps) load(s + S - 1, slot == 0 ? S - 1 : slot - 1);
+      if ((g0 + s + 1) * kGranule > a.K) {
+        // what the weights have behind the end of K becomes 0
 #pragma unroll
-      for (int d = 0; d < D; ++d) {
+        for (int j = 0; j < 2 * NT; ++j) {
+          const int piece = (lane & 7) ^ ((8 * j + (lane >> 3)) / 2 & 7);
+          if ((g0 + s) * kGranule + piece * 16 >= a.K)
+            *reinterpret_cast<i32x4*>(mine + slot * kStage + j * 8 * kGranule + lane * 16) =
+                i32x4{0, 0, 0, 0};
+        }
+      }
+      const char* at = mine + slot * kStage + m * kGranule;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < 2; ++u) {
+        const int place = ((4 * u + kq) ^ (m >> 1)) * 16;
+        i32x4 w[NT];
+#pragma unroll
+        for (int h = 0; h < NT; ++h)
+          w[h] = *reinterpret_cast<const i32x4*>(at + h * 16 * kGranule + place);
+#pragma unroll
+        for (int q = 0; q < MT; ++q) {
+          const i32x4 x =
+              *reinterpret_cast<const i32x4*>(at + (NT + q) * 16 * kGranule + place);
 #pragma unroll
           for (int h = 0; h < NT; ++h)
-#pragma unroll
-            for (int q = 0; q < MT; ++q)
-              acc[h][q] =
-                  __builtin_amdgcn_mfma_i32_16x16x64_i8(w[d][u][h], x[d][u][q], acc[h][q], 0, 0, 0);
-        load(d, s0 + d + D);
+            acc[h][q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[h], x, acc[h][q], 0, 0, 0);
+        }
       }
+      slot = slot == S - 1 ? 0 : slot + 1;
     }
+    __syncthreads();  // every wave is done with its granules
 #pragma unroll
     for (int h = 0; h < NT; ++h)
 #pragma unroll
@@ -205,31 +257,26 @@ __global__ __launch_bounds__(W * kWave) void product_few(Int8Args a) {
         for (int r = 0; r < 4; ++r) part[wave][(h * MT + q) * 4 + r][lane] = acc[h][q][r];
     __syncthreads();
     // a wave adds up the elements `at` of every fragment: lane (m, kq) holds row
-    // 16 q + m and column 4 kq + r
+    // 16 q + m and weight row 4 kq + r of each tile
     for (int at = wave; at < MT * 4; at += W) {
       const int q = at / 4, r = at % 4;
       const int row = 16 * q + m;
+      auto sum = [&](int h, int l) {
+        int v = 0;
+#pragma unroll
+        for (int o = 0; o < W; ++o) v += part[o][(h * MT + q) * 4 + r][l];
+        return float(v);
+      };
       const float xs = row < nr ? a.row_scale[row0 + row] : 0.0f;
-      float y[NT];
+      const float* ws = a.w_scale + int64_t(e) * a.N;
+      __bf16* to = reinterpret_cast<__bf16*>(a.out) + (row0 + row) * a.wide;
 #pragma unroll
-      for (int h = 0; h < NT; ++h) {
-        int sum = 0;
-#pragma unroll
-        for (int v = 0; v < W; ++v) sum += part[v][(h * MT + q) * 4 + r][lane];
-        const int n = (kSwiglu ? n0 : n0 + 16 * h) + 4 * kq + r;
-        const float ws =
-            n < limit ? a.w_scale[int64_t(e) * a.N + n + (kSwiglu ? h * half : 0)] : 0.0f;
-        y[h] = float(sum) * xs * ws;
-      }
-      if (row < nr) {
-        __bf16* to = reinterpret_cast<__bf16*>(a.out) + (row0 + row) * a.wide;
-        if (kSwiglu) {
-          if (n0 + 4 * kq + r < limit) to[n0 + 4 * kq + r] = __bf16(swiglu(y[0], y[NT - 1]));
-        } else {
-#pragma unroll
-          for (int h = 0; h < NT; ++h)
-            if (n0 + 16 * h + 4 * kq + r < limit) to[n0 + 16 * h + 4 * kq + r] = __bf16(y[h]);
-        }
+      for (int h = 0; h < (kSwiglu ? 1 : NT); ++h) {
+        const int n = n0 + 16 * h + 4 * kq + r;
+        if (row >= nr || n >= limit || (kMixed && kq >= 2)) continue;
+        float y = sum(h, lane) * xs * ws[n];
+        if (kSwiglu) y = swiglu(y, sum(NT - 1, kMixed ? lane + 32 : lane) * xs * ws[half + n]);
+        to[n] = __bf16(y);
       }
     }
     __syncthreads();
@@ -240,16 +287,22 @@ __global__ __launch_bounds__(W * kWave) void product_few(Int8Args a) {
 
 // BM rows and BN weight rows, by WM x WN waves, in 32x32x32 MFMAs; with SwiGLU
 // tiles of 32 gates alternate with the 32 other factors that they meet.
-template <bool kSwiglu, int BM, int BN, int WM, int WN, int S>
+template <bool kSwiglu, int BM, int BN, int WM, int WN, int S, int P>
 __global__ __launch_bounds__(WM * WN * kWave) void product_tile(Int8Args a) {
   constexpr int W = WM * WN;
   constexpr int MT = BM / WM / 32, NT = BN / WN / 32;
   static_assert(BM == WM * MT * 32 && BN == WN * NT * 32 && (!kSwiglu || NT % 2 == 0), "tiles");
+
   static_assert(W % 2 == 0 && BM % (8 * W) == 0 && BN % (8 * W) == 0, "8 rows a load of a wave");
   constexpr int LW = BN / (8 * W), LX = BM / (8 * W), L = LW + LX;  // loads of a wave
+  static_assert(L <= 4 * NT * MT, "a load an MFMA");
   constexpr int kStage = (BM + BN) * kGranule;
   constexpr int kCols = kSwiglu ? BN / 2 : BN;
-  __shared__ __align__(16) char lds[S * kStage];
+  // a row of results is 16 bytes longer than it needs to be: 32 rows' same columns
+  // then lie in different banks
+  constexpr int kPitch = kCols * 2 + 16;
+  constexpr int kRoom = S * kStage > BM * kPitch ? S * kStage : BM * kPitch;
+  __shared__ __align__(16) char lds[kRoom];
   const int lane = lane_id(), wave = wave_in_block();
   const int wm = wave / WN, wn = wave % WN;
   const int half = a.N / 2, limit = kSwiglu ? half : a.N;
@@ -278,15 +331,13 @@ __global__ __launch_bounds__(WM * WN * kWave) void product_tile(Int8Args a) {
       const int c = j >= LW ? r : kSwiglu ? r / 64 * 32 + r % 32 : r;
       from[j] = offset_if(c < (j < LW ? held : nr), c * a.K + piece * 16);
     }
-    auto load = [&](int s, int slot) {
-#pragma unroll
-      for (int j = 0; j < L; ++j) {
-        const int tile = 8 * (j * W + wave);  // the first row it fills
-        const buffer& b = j >= LW ? xb : kSwiglu && tile / 32 % 2 == 1 ? wu : wg;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            b, (__attribute__((address_space(3))) void*)(lds + slot * kStage + tile * kGranule), 16,
-            int(uint32_t(from[j]) + uint32_t(s * kGranule)), 0, 0, 0);
-      }
+    // Load j of step s; past the last step one that reads nothing, so that every
+    // step has as many on their way.
+    auto load = [&](int j, int s, int slot) {
+      const int tile = 8 * (j * W + wave);  // the first row it fills
+      const buffer& b = j >= LW ? xb : kSwiglu && tile / 32 % 2 == 1 ? wu : wg;
+      const uint32_t at = s < steps ? s * kGranule : 0x70000000u;
+      load_to_lds(b, lds + slot * kStage + tile * kGranule, int(uint32_t(from[j]) + at));
     };
 
     i32x16 acc[NT][MT];
@@ -300,74 +351,128 @@ __global__ __launch_bounds__(WM * WN * kWave) void product_tile(Int8Args a) {
     const int swz = (lane >> 1) & 7, hi = lane >> 5;
     const int wrow = (wn * NT * 32 + (lane & 31)) * kGranule;
     const int xrow = (BN + wm * MT * 32 + (lane & 31)) * kGranule;
-    // kEnd: the last step where K ends inside it; what lies behind is masked in
-    // one of the operands.
-    auto multiply = [&](int s, int slot, bool end) {
-      const char* at = lds + slot * kStage;
+    // The operands of one MFMA step (32 values of K) of a slot.
+    i32x4 w[4][NT], x[4][MT];
+    auto read = [&](int slot, int kk) {
+      const char* at = lds + slot * kStage + ((2 * kk + hi) ^ swz) * 16;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const int place = ((2 * kk + hi) ^ swz) * 16;
-        i32x4 w[NT], x[MT];
+      for (int h = 0; h < NT; ++h)
+        w[kk][h] = *reinterpret_cast<const i32x4*>(at + wrow + h * 32 * kGranule);
 #pragma unroll
-        for (int h = 0; h < NT; ++h)
-          w[h] = *reinterpret_cast<const i32x4*>(at + wrow + h * 32 * kGranule + place);
-#pragma unroll
-        for (int q = 0; q < MT; ++q)
-          x[q] = *reinterpret_cast<const i32x4*>(at + xrow + q * 32 * kGranule + place);
-        if (end) {
-          const bool in = s * kGranule + (2 * kk + hi) * 16 < a.K;
-#pragma unroll
-          for (int q = 0; q < MT; ++q)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[q][r] = in ? x[q][r] : 0;
-        }
-#pragma unroll
-        for (int h = 0; h < NT; ++h)
-#pragma unroll
-          for (int q = 0; q < MT; ++q)
-            acc[h][q] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[h], x[q], acc[h][q], 0, 0, 0);
-      }
+      for (int q = 0; q < MT; ++q)
+        x[kk][q] = *reinterpret_cast<const i32x4*>(at + xrow + q * 32 * kGranule);
     };
 
 #pragma unroll
     for (int s = 0; s < S - 1; ++s)
-      if (s < steps) load(s, s);
-    int slot = 0;
-    for (int s = 0; s < steps; ++s) {
-      // the loads of this step have come when at most those of the later ones
-      // are on their way
-      if (S > 2 && s + S - 2 < steps)
-        asm volatile("s_waitcnt vmcnt(%0)" ::"i"((S - 2) * L) : "memory");
-      else
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+      for (int j = 0; j < L; ++j) load(j, s, s);
+    // One step's end of the waiting: its loads have come when only those of the
+    // later steps are on their way, and the reads of the slot that is filled next
+    // are done.
+    auto arrive = [&](int s, int slot) {
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"((S - 2) * L) : "memory");
+      if (s == steps - 1 && a.K % kGranule != 0) {
+        // what the rows have behind the end of K becomes 0, each piece by the
+        // lane that has loaded it
+        if (s * kGranule + piece * 16 >= a.K) {
+#pragma unroll
+          for (int j = LW; j < L; ++j)
+            *reinterpret_cast<i32x4*>(lds + slot * kStage + 8 * (j * W + wave) * kGranule +
+                                      lane * 16) = i32x4{0, 0, 0, 0};
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      }
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      const int next = slot == 0 ? S - 1 : slot - 1;
-      if (s + S - 1 < steps) load(s + S - 1, next);
-      multiply(s, slot, s == steps - 1 && a.K % kGranule != 0);
-      slot = slot == S - 1 ? 0 : slot + 1;
-    }
-
-    // lane: row lane % 32, columns 8 (r / 4) + 4 (lane / 32) + r % 4 of each tile
+    };
+    int slot = 0;
+    if (wm * MT * 32 >= nr) {
+      // waves whose rows are all behind the chunk's only load. (A loop of their own:
+      // a branch around the MFMAs moved the accumulators at every step, 1,320
+      // cycles a step of the form of 64 rows and 128 weight rows instead of 1,000.)
+      for (int s = 0; s < steps; ++s) {
+        arrive(s, slot);
 #pragma unroll
-    for (int q = 0; q < MT; ++q) {
-      const int row = (wm * MT + q) * 32 + (lane & 31);
-      if (row < nr) {
-        const float xs = a.row_scale[row0 + row];
-        __bf16* to = reinterpret_cast<__bf16*>(a.out) + (row0 + row) * a.wide;
+        for (int j = 0; j < L; ++j) load(j, s + S - 1, slot == 0 ? S - 1 : slot - 1);
+        slot = slot == S - 1 ? 0 : slot + 1;
+      }
+    } else {
+      for (int s = 0; s < steps; ++s) {
+        arrive(s, slot);
+        const int next = slot == 0 ? S - 1 : slot - 1;
+        // The operands of the MFMAs are read P steps ahead of them, and the loads
+        // are issued between MFMAs: all at once they hold the wave up.
 #pragma unroll
-        for (int h = 0; h < NT; h += kSwiglu ? 2 : 1) {
+        for (int kk = 0; kk < P; ++kk) read(slot, kk);
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int n = n0 + (wn * NT + h) / (kSwiglu ? 2 : 1) * 32 + 8 * (r / 4) + 4 * hi + r % 4;
-            if (n < limit) {
-              const float* ws = a.w_scale + int64_t(e) * a.N + n;
-              float y = float(acc[h][q][r]) * xs * ws[0];
-              if (kSwiglu) y = swiglu(y, float(acc[(h + 1) % NT][q][r]) * xs * ws[half]);
-              to[n] = __bf16(y);
+        for (int kk = 0; kk < 4; ++kk) {
+          if (kk + P < 4) read(slot, kk + P);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int h = 0; h < NT; ++h)
+#pragma unroll
+            for (int q = 0; q < MT; ++q) {
+              acc[h][q] =
+                  __builtin_amdgcn_mfma_i32_32x32x32_i8(w[kk][h], x[kk][q], acc[h][q], 0, 0, 0);
+              // one load behind each MFMA till all are issued
+              const int j = (kk * NT + h) * MT + q;
+              if (j < L) {
+                __builtin_amdgcn_sched_barrier(0);
+                load(j, s + S - 1, next);
+                __builtin_amdgcn_sched_barrier(0);
+              }
             }
-          }
         }
+        slot = slot == S - 1 ? 0 : slot + 1;
+      }
+    }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+
+    // The results leave through LDS, so that rows are stored whole: written as
+    // they lie in the accumulators they were 16 bytes of 32 rows an instruction.
+    // Lane: row lane % 32, columns 8 (r / 4) + 4 (lane / 32) + r % 4 of each tile.
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < NT; h += kSwiglu ? 2 : 1) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int c = (wn * NT + h) / (kSwiglu ? 2 : 1) * 32 + 8 * g + 4 * hi;
+        float ws[2][4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float* p = a.w_scale + int64_t(e) * a.N + min(n0 + c + r, limit - 1);
+          ws[0][r] = p[0];
+          ws[1][r] = kSwiglu ? p[half] : 0.0f;
+        }
+#pragma unroll
+        for (int q = 0; q < MT; ++q) {
+          const int row = (wm * MT + q) * 32 + (lane & 31);
+          const float xs = a.row_scale[row0 + min(row, nr - 1)];
+          bf16x4 y;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float v = float(acc[h][q][4 * g + r]) * xs * ws[0][r];
+            if (kSwiglu) v = swiglu(v, float(acc[(h + 1) % NT][q][4 * g + r]) * xs * ws[1][r]);
+            y[r] = __bf16(v);
+          }
+          *reinterpret_cast<bf16x4*>(lds + row * kPitch + c * 2) = y;
+        }
+      }
+    }
+    __syncthreads();
+    __bf16* to = reinterpret_cast<__bf16*>(a.out) + row0 * a.wide + n0;
+    constexpr int kPieces = kCols / 8;  // of 16 bytes, a row
+    for (int at = threadIdx.x; at < nr * kPieces; at += W * kWave) {
+      const int row = at / kPieces, c = at % kPieces * 8;
+      const bf16x8 y = *reinterpret_cast<const bf16x8*>(lds + row * kPitch + c * 2);
+      __bf16* p = to + int64_t(row) * a.wide + c;
+      if (a.wide % 8 == 0 && c + 8 <= held) {
+        *reinterpret_cast<bf16x8*>(p) = y;
+      } else {
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (c + r < held) p[r] = y[r];
       }
     }
     __syncthreads();  // LDS is written anew when every wave is done with it
@@ -376,31 +481,68 @@ __global__ __launch_bounds__(WM * WN * kWave) void product_tile(Int8Args a) {
 
 // ---------------------------------------------------------------------------
 
-// Forms: rows and columns of weights (with SwiGLU two weight rows a column)
-// that a workgroup takes, its waves.
+// Forms of the two kernels, and what each takes. A launch's time goes in rounds:
+// every CU takes per_cu workgroups at a time, and a round with at most one for
+// each CU, or else with two, takes fixed + step * (steps of 128 values) ns.
 struct Form {
-  int rows, weights, waves;
+  int rows, weights;  // of a workgroup (with SwiGLU two weight rows make a column)
+  int waves, over_k;  // its waves, and how many parts they cut K into
+  int per_cu;
+  int fixed1, step1, fixed2, step2;
 };
-constexpr Form kForms[] = {{16, 32, 8}, {32, 32, 8}, {64, 32, 8}, {128, 128, 4}, {256, 256, 8}};
+
+// The times are fitted to 500 measured ones: rows from 1 to 8,192, plain and of 2 to
+// 48 experts, K from 1,024 to 7,168, N from 1,024 to 7,168. Chosen by them, a launch
+// takes 1.5% more than in the form that was the fastest there, 25% at most. Every
+// form is the best of some sizes by 20% and more (K = 5,120, N = 4,096 with SwiGLU: 24
+// rows 6.8 us in form 0 and 7.9 in the next; 64 rows 8.2 in form 1, 11.1 in form 2, 18.4 in form
+// 4; 128 rows 11.2 in form 2, 13.8 and 14.8 around it; 256 rows 15.2 in form 3, 19.2 and 19.0
+// around it; 512 rows 20.0 in form 4, 35.6 in the next; 1,300 rows 40.8 in form 5, 45.8 and 59.3
+// around it; 4,093 rows 83 in form 6, 93 in form 5).
+constexpr Form kForms[] = {
+    {32, 16, 8, 8, 1, 1470, 530, 0, 0},        {32, 32, 4, 4, 1, 1840, 400, 0, 0},
+    {64, 32, 4, 4, 1, 2640, 615, 0, 0},        {64, 64, 2, 1, 2, 3240, 220, 2590, 460},
+    {64, 128, 4, 1, 2, 2330, 325, 3690, 680},  {128, 128, 4, 1, 2, 2650, 735, 5060, 1000},
+    {256, 256, 8, 1, 1, 10230, 1200, 0, 0},
+};
+constexpr int kFormCount = sizeof(kForms) / sizeof(kForms[0]);
 
 template <bool kSwiglu>
 void launch(int form, dim3 grid, hipStream_t st, const Int8Args& a) {
   const int threads = kForms[form].waves * kWave;
   switch (form) {
-    case 0: product_few<kSwiglu, 1, 2, 8, 4><<<grid, threads, 0, st>>>(a); break;
-    case 1: product_few<kSwiglu, 2, 2, 8, 3><<<grid, threads, 0, st>>>(a); break;
-    case 2: product_few<kSwiglu, 4, 2, 8, 2><<<grid, threads, 0, st>>>(a); break;
-    case 3: product_tile<kSwiglu, 128, 128, 2, 2, 2><<<grid, threads, 0, st>>>(a); break;
-    default: product_tile<kSwiglu, 256, 256, 2, 4, 2><<<grid, threads, 0, st>>>(a);
+    case 0: product_few<kSwiglu, 2, 1, 8, 3><<<grid, threads, 0, st>>>(a); break;
+    case 1: product_few<kSwiglu, 2, 2, 4, 3><<<grid, threads, 0, st>>>(a); break;
+    case 2: product_few<kSwiglu, 4, 2, 4, 3><<<grid, threads, 0, st>>>(a); break;
+    case 3: product_tile<kSwiglu, 64, 64, 2, 1, 4, 2><<<grid, threads, 0, st>>>(a); break;
+    case 4: product_tile<kSwiglu, 64, 128, 2, 2, 3, 2><<<grid, threads, 0, st>>>(a); break;
+    case 5: product_tile<kSwiglu, 128, 128, 2, 2, 2, 1><<<grid, threads, 0, st>>>(a); break;
+    default: product_tile<kSwiglu, 256, 256, 2, 4, 2, 1><<<grid, threads, 0, st>>>(a);
   }
 }
 
-// By the mean number of rows of an expert that has any (uniform routing at worst).
-int form_of(int64_t mean, int64_t tiles256) {
-  if (mean <= 16) return 0;
-  if (mean <= 32) return 1;
-  if (mean <= 64) return 2;
-  return tiles256 < 200 ? 3 : 4;
+int64_t column_tiles(const Form& f, int N) { return (N + f.weights - 1) / f.weights; }
+
+// The time of a form in ns, for `pairs` rows of `active` experts; an expert's last
+// chunk is half full on average.
+int64_t time_of(const Form& f, int64_t pairs, int64_t active, int N, int K) {
+  const int64_t chunks = active == 1 ? (pairs + f.rows - 1) / f.rows
+                                     : std::max(active, pairs / f.rows + active / 2);
+  const int64_t granules = (K + kGranule - 1) / kGranule;
+  const int64_t steps = (granules + f.over_k - 1) / f.over_k;
+  const int64_t tiles = chunks * column_tiles(f, N), round = int64_t(256) * f.per_cu;
+  const int64_t full = tiles / round, rest = tiles % round;
+  const int64_t one = f.fixed1 + f.step1 * steps, two = f.fixed2 + f.step2 * steps;
+  if (f.per_cu == 1) return (full + (rest > 0)) * one;
+  return full * two + (rest > 256 ? two : rest > 0 ? one : 0);
+}
+
+int form_of(int64_t pairs, int64_t active, int N, int K) {
+  int best = 0;
+  for (int f = 1; f < kFormCount; ++f)
+    if (time_of(kForms[f], pairs, active, N, K) < time_of(kForms[best], pairs, active, N, K))
+      best = f;
+  return best;
 }
 
 }  // namespace
@@ -425,14 +567,11 @@ int moe_int8_product(const moe_shape_t* shape, int N, int act, const int8_t* row
       !aligned(row_scale, 4) || !aligned(expert_counts, 4) || !aligned(expert_offsets, 4))
     return MOE_ERR_ARG;
   const bool swiglu = act == MOE_ACT_SWIGLU;
-  const int64_t active = std::min<int64_t>(shape->E, pairs), mean = (pairs + active - 1) / active;
-  auto most = [&](const Form& f) {  // chunks, at most, and column tiles
-    const int64_t chunks = active + (pairs - active) / f.rows;
-    return std::pair<int64_t, int64_t>(chunks, (N + f.weights - 1) / f.weights);
-  };
-  const auto big = most(kForms[4]);
-  const int form = form_of(mean, (pairs + 255) / 256 * big.second);
-  const auto [chunks, tiles] = most(kForms[form]);
+  const int64_t active = std::min<int64_t>(shape->E, pairs);
+  const int form = form_of(pairs, active, N, shape->H);
+  // chunks of the experts' rows, at most, and tiles of the weights' columns
+  const int64_t chunks = active + (pairs - active) / kForms[form].rows;
+  const int64_t tiles = column_tiles(kForms[form], N);
   const Int8Args a{rows, row_scale, expert_counts, expert_offsets, w_q, w_scale, out, err_word,
                    cap_expert, int(pairs), shape->E, shape->H, N, swiglu ? N / 2 : N, int(tiles)};
   const dim3 grid(uint32_t(std::min<int64_t>(chunks * tiles, kMostGroups)));
