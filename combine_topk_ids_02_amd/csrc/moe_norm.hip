@@ -2,10 +2,17 @@
 // kernels for CDNA4 (gfx950, wave64) behind include/moe_dispatch.h.
 //
 // All three are one pass over their rows: a row lies in the registers of W
-// waves (pieces of 8 values, NC of them a lane), is read once in 16-byte loads
-// that are all on their way before the first is used, and its sum or maximum
-// is joined through DPP and, with W > 1, 64 bytes of LDS. What bounds them is
-// the memory: few bytes a value are computed on.
+// waves (pieces of 4 or 8 values, NC of them a lane), is read once in loads that are
+// all on their way before the first is used, and its sum or maximum is joined
+// through DPP and, with W > 1, 64 bytes of LDS. What bounds them is the memory:
+// few operations a value. Measured (kernel time, three sets of buffers in turn):
+//  - norm, 4,093 x 5,120 in bf16 to bf16 and MXFP8 (189 MB) 29.5 us, 6.4 TB/s; 8,192 x
+//    7,168 with a float32 stream (705 MB) 123 us, 5.7 TB/s; one row of 5,120 3.4 us;
+//  - its gradient, 8,192 x 7,168 with a float32 stream (940 MB) 179 us, 5.2 TB/s (512
+//    workgroups of 14 waves; 256 173 us, but 8,192 x 5,120 in bf16 82 instead of 70;
+//    a row's loads before the row ahead is done: 185);
+//  - rows to int8, 24,576 of 2,048 (151 MB) 29.5 us, 5.1 TB/s.
+// A copy of 1 GiB on this card takes its bytes at 5.1 TB/s.
 
 #include "moe_common.h"
 
@@ -16,68 +23,112 @@ using namespace moe;
 typedef uint32_t vec2 __attribute__((ext_vector_type(2)));
 typedef uint32_t vec4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short short2v __attribute__((ext_vector_type(2)));
 
-constexpr int kPiece = 8;           // values of a row that a lane takes at once
+// Values of a row that a lane takes at once: 16 bytes of the stream, so that an
+// instruction reads and writes whole cache lines (8 values of float32, two pieces of
+// 16 bytes, made half lines of each: 8,192 x 7,168 130 us, with 4 123).
+template <bool kF32>
+constexpr int kPieceOf = kF32 ? 4 : 8;
 constexpr int kMostRow = 1 << 16;   // values of a row of the quantiser
 constexpr int kMostNorm = 1 << 15;  // and of the norm and its gradient
 constexpr int kMostWaves = 16;      // waves of a workgroup
 constexpr int kMostGroups = 1 << 21;
 
-struct Row8 {
-  float v[kPiece];
+// N values of a row: what a lane takes at once.
+template <int N>
+struct Row {
+  float v[N];
 };
 
-__device__ __forceinline__ Row8 widen(bf16x8 p) {
-  Row8 r;
+template <int N>
+struct Bf16;
+template <>
+struct Bf16<4> {
+  typedef bf16x4 type;
+};
+template <>
+struct Bf16<8> {
+  typedef bf16x8 type;
+};
+
+template <int N>
+__device__ __forceinline__ Row<N> widen(typename Bf16<N>::type p) {
+  Row<N> r;
 #pragma unroll
-  for (int i = 0; i < kPiece; ++i) r.v[i] = float(p[i]);
+  for (int i = 0; i < N; ++i) r.v[i] = float(p[i]);
   return r;
 }
 
-__device__ __forceinline__ bf16x8 narrow(const Row8& r) {
-  bf16x8 p;
+template <int N>
+__device__ __forceinline__ typename Bf16<N>::type narrow(const Row<N>& r) {
+  typename Bf16<N>::type p;
 #pragma unroll
-  for (int i = 0; i < kPiece; ++i) p[i] = __bf16(r.v[i]);
+  for (int i = 0; i < N; ++i) p[i] = __bf16(r.v[i]);
   return p;
 }
 
-// Piece `at` (in pieces) of a tensor of bf16 or of float32.
-template <bool kF32>
+// Piece `at` (of N values each) of a tensor of bf16 or of float32.
+template <bool kF32, int N>
 struct Piece;
-template <>
-struct Piece<false> {
-  bf16x8 p;
+template <int N>
+struct Piece<false, N> {
+  typename Bf16<N>::type p;
   __device__ __forceinline__ void load(const void* t, int64_t at) {
-    p = static_cast<const bf16x8*>(t)[at];
+    p = static_cast<const typename Bf16<N>::type*>(t)[at];
   }
-  __device__ __forceinline__ Row8 get() const { return widen(p); }
+  __device__ __forceinline__ Row<N> get() const { return widen<N>(p); }
 };
-template <>
-struct Piece<true> {
-  f32x4 p[2];
+template <int N>
+struct Piece<true, N> {
+  f32x4 p[N / 4];
   __device__ __forceinline__ void load(const void* t, int64_t at) {
-    p[0] = static_cast<const f32x4*>(t)[2 * at];
-    p[1] = static_cast<const f32x4*>(t)[2 * at + 1];
-  }
-  __device__ __forceinline__ Row8 get() const {
-    Row8 r;
 #pragma unroll
-    for (int i = 0; i < kPiece; ++i) r.v[i] = p[i / 4][i % 4];
+    for (int i = 0; i < N / 4; ++i) p[i] = static_cast<const f32x4*>(t)[N / 4 * at + i];
+  }
+  __device__ __forceinline__ Row<N> get() const {
+    Row<N> r;
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.v[i] = p[i / 4][i % 4];
     return r;
   }
 };
 
-template <bool kF32>
-__device__ __forceinline__ void store_piece(void* t, int64_t at, const Row8& r) {
+template <typename V, bool kStream>
+__device__ __forceinline__ void store(void* t, int64_t at, const V& v) {
+  if (kStream)
+    __builtin_nontemporal_store(v, static_cast<V*>(t) + at);
+  else
+    static_cast<V*>(t)[at] = v;
+}
+
+// kStream: nontemporal, for what this kernel does not read again (4,093 x 5,120 in
+// bf16 with MXFP8 codes 37 us without, 29 us with).
+template <bool kF32, bool kStream, int N>
+__device__ __forceinline__ void store_piece(void* t, int64_t at, const Row<N>& r) {
   if (kF32) {
-    f32x4* to = static_cast<f32x4*>(t) + 2 * at;
-    to[0] = f32x4{r.v[0], r.v[1], r.v[2], r.v[3]};
-    to[1] = f32x4{r.v[4], r.v[5], r.v[6], r.v[7]};
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      store<f32x4, kStream>(t, N / 4 * at + i,
+                            f32x4{r.v[4 * i], r.v[4 * i + 1], r.v[4 * i + 2], r.v[4 * i + 3]});
   } else {
-    static_cast<bf16x8*>(t)[at] = narrow(r);
+    store<typename Bf16<N>::type, kStream>(t, at, narrow<N>(r));
   }
+}
+
+// Codes of N values, a byte each.
+template <int N>
+struct Codes {
+  uint32_t w[N / 4];
+};
+
+__device__ __forceinline__ void store_codes(void* t, int64_t at, const Codes<8>& c) {
+  store<vec2, true>(t, at, vec2{c.w[0], c.w[1]});
+}
+__device__ __forceinline__ void store_codes(void* t, int64_t at, const Codes<4>& c) {
+  store<uint32_t, true>(t, at, c.w[0]);
 }
 
 // A value's magnitude as bits, which order as the magnitudes do, an infinity
@@ -137,21 +188,22 @@ struct Int8Scale {
     scale = finite ? t / 127.0f : __uint_as_float(0x7FC00000u);
     factor = finite && top > 0 ? 127.0f * (1.0f / (t * move)) : 0.0f;
   }
-  __device__ __forceinline__ vec2 codes(Row8 r) const {
-    vec2 q = {0, 0};
+  template <int N>
+  __device__ __forceinline__ Codes<N> codes(Row<N> r) const {
+    Codes<N> q = {};
     if (factor == 0.0f) return q;  // uniform, as `move` is
     if (move != 1.0f) {
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) r.v[i] *= move;
+      for (int i = 0; i < N; ++i) r.v[i] *= move;
     }
 #pragma unroll
-    for (int i = 0; i < kPiece; ++i)
-      q[i / 4] |= uint32_t(int(__builtin_rintf(r.v[i] * factor)) & 0xFF) << (i % 4 * 8);
+    for (int i = 0; i < N; ++i)
+      q.w[i / 4] |= uint32_t(int(__builtin_rintf(r.v[i] * factor)) & 0xFF) << (i % 4 * 8);
     return q;
   }
 };
 
-// Eight float32 divided by a power of two and rounded to e4m3 by the scaled
+// Four float32 divided by a power of two and rounded to e4m3 by the scaled
 // conversion (nearest, ties to even). It turns a magnitude that rounds past 448
 // into NaN (0x7F with the sign); among finite values that can only be such an
 // overflow, so those bytes are lowered by one, to +-448.
@@ -165,28 +217,29 @@ __device__ __forceinline__ uint32_t e4m3x4(const float* v, float scale) {
 }
 
 // MXFP8 codes of a lane's piece and the scale byte of its block of 32 values,
-// which four neighbouring lanes hold (a block has all four or none).
-__device__ __forceinline__ vec2 mxfp8_codes(const Row8& r, uint32_t* scale_byte) {
+// which 32 / N neighbouring lanes hold (all of a block, or none).
+template <int N>
+__device__ __forceinline__ Codes<N> mxfp8_codes(const Row<N>& r, uint32_t* scale_byte) {
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < kPiece; ++i) top = max(top, magnitude(r.v[i]));
+  for (int i = 0; i < N; ++i) top = max(top, magnitude(r.v[i]));
   top = max(top, dpp_bits<0xB1>(top));  // lanes 1 0 3 2 of each four
   top = max(top, dpp_bits<0x4E>(top));  // lanes 2 3 0 1
-  vec2 q;
+  if (N == 4) top = max(top, dpp_bits<0x141>(top));  // each eight lanes in reverse
+  Codes<N> q = {};
   if (top >= 0x7F800000u) {  // NaN codes with the value's sign
     *scale_byte = 0xFF;
-    q = vec2{0, 0};
 #pragma unroll
-    for (int i = 0; i < kPiece; ++i)
-      q[i / 4] |= ((__float_as_uint(r.v[i]) >> 24 & 0x80u) | 0x7Fu) << (i % 4 * 8);
+    for (int i = 0; i < N; ++i)
+      q.w[i / 4] |= ((__float_as_uint(r.v[i]) >> 24 & 0x80u) | 0x7Fu) << (i % 4 * 8);
     return q;
   }
   // floor(log2(top)) - 8, at least -127: a subnormal top is below that anyway
   const int e = max(-127, int(top >> 23) - 127 - 8);
   *scale_byte = uint32_t(e + 127);
   const float scale = __uint_as_float(uint32_t(e + 127) << 23);  // E8M0 byte as an exponent
-  q[0] = e4m3x4(r.v, scale);
-  q[1] = e4m3x4(r.v + 4, scale);
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) q.w[i] = e4m3x4(r.v + 4 * i, scale);
   return q;
 }
 
@@ -215,13 +268,14 @@ __global__ __launch_bounds__(kMostWaves * kWave) void norm_rows(NormArgs a) {
   __shared__ float part[2][kMostWaves];
   __shared__ uint32_t tops[2][kMostWaves];
   const int waves = blockDim.x / kWave, wave = wave_in_block();
-  const int pieces = a.H / kPiece;
+  constexpr int N = kPieceOf<kF32>;
+  const int pieces = a.H / N;
   int turn = 0;
   for (int row = blockIdx.x; row < a.T; row += gridDim.x, turn ^= 1) {
     const int64_t at0 = int64_t(row) * pieces;
-    Piece<false> x[NC];
-    Piece<kF32> res[NC];
-    Piece<kWeightF32> w[NC];
+    Piece<false, N> x[NC];
+    Piece<kF32, N> res[NC];
+    Piece<kWeightF32, N> w[NC];
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int p = i * blockDim.x + threadIdx.x;
@@ -231,7 +285,7 @@ __global__ __launch_bounds__(kMostWaves * kWave) void norm_rows(NormArgs a) {
         w[i].load(a.weight, p);
       }
     }
-    Row8 h[NC];
+    Row<N> h[NC];
     float squares = 0.0f;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
@@ -239,14 +293,14 @@ __global__ __launch_bounds__(kMostWaves * kWave) void norm_rows(NormArgs a) {
       if (p < pieces) {
         h[i] = x[i].get();
         if (a.residual) {
-          const Row8 r = res[i].get();
+          const Row<N> r = res[i].get();
 #pragma unroll
-          for (int j = 0; j < kPiece; ++j) h[i].v[j] += r.v[j];
-          if (!kF32) h[i] = widen(narrow(h[i]));
-          store_piece<kF32>(a.sum, at0 + p, h[i]);
+          for (int j = 0; j < N; ++j) h[i].v[j] += r.v[j];
+          if (!kF32) h[i] = widen<N>(narrow<N>(h[i]));
+          store_piece<kF32, true>(a.sum, at0 + p, h[i]);
         }
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) squares = fmaf(h[i].v[j], h[i].v[j], squares);
+        for (int j = 0; j < N; ++j) squares = fmaf(h[i].v[j], h[i].v[j], squares);
       }
     }
     const float total = join_sum(squares, part[turn], wave, waves);
@@ -257,17 +311,18 @@ __global__ __launch_bounds__(kMostWaves * kWave) void norm_rows(NormArgs a) {
     for (int i = 0; i < NC; ++i) {
       const int p = i * blockDim.x + threadIdx.x;
       if (p < pieces) {
-        const Row8 g = w[i].get();
+        const Row<N> g = w[i].get();
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) {
+        for (int j = 0; j < N; ++j) {
           h[i].v[j] = h[i].v[j] * inv * g.v[j];
           if (kFmt == kInt8) top = max(top, magnitude(h[i].v[j]));
         }
-        if (a.out) store_piece<false>(a.out, at0 + p, h[i]);
+        if (a.out) store_piece<false, true>(a.out, at0 + p, h[i]);
         if (kFmt == kMxfp8) {
           uint32_t byte;
-          static_cast<vec2*>(a.q)[at0 + p] = mxfp8_codes(h[i], &byte);
-          if (p % 4 == 0) static_cast<uint8_t*>(a.q_scale)[(at0 + p) / 4] = uint8_t(byte);
+          store_codes(a.q, at0 + p, mxfp8_codes(h[i], &byte));
+          if (p % (32 / N) == 0)
+            static_cast<uint8_t*>(a.q_scale)[(at0 + p) / (32 / N)] = uint8_t(byte);
         }
       }
     }
@@ -276,7 +331,7 @@ __global__ __launch_bounds__(kMostWaves * kWave) void norm_rows(NormArgs a) {
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int p = i * blockDim.x + threadIdx.x;
-        if (p < pieces) static_cast<vec2*>(a.q)[at0 + p] = s.codes(h[i]);
+        if (p < pieces) store_codes(a.q, at0 + p, s.codes(h[i]));
       }
       if (threadIdx.x == 0) static_cast<float*>(a.q_scale)[row] = s.scale;
     }
@@ -294,103 +349,135 @@ struct NormGradArgs {
   void* d_res;
   float* part;  // [gridDim.x][H]: each workgroup's share of the weight's gradient, or NULL
   int T, H;
+  int waves, at_once;  // waves a row, rows a workgroup
 };
 
 // With g = d_out * w and unit = h * inv: d_h = inv * (g - unit * mean(g * unit))
-// + d_sum. A workgroup takes every gridDim.x-th row and keeps the sum of d_out *
-// unit over them in registers; norm_grad_join adds up the workgroups' in a fixed
-// order.
+// + d_sum. A workgroup takes `at_once` rows at a time, W waves each, and keeps the
+// sums of d_out * unit in registers; at the end its rows' meet in LDS, one after
+// the other, and norm_grad_join adds up the workgroups' in a fixed order.
 template <bool kF32, bool kWeightF32, int NC>
 __global__ __launch_bounds__(kMostWaves * kWave) void norm_grad(NormGradArgs a) {
+  constexpr int N = kPieceOf<kF32>;
   __shared__ float part[2][kMostWaves];
-  const int waves = blockDim.x / kWave, wave = wave_in_block();
-  const int pieces = a.H / kPiece;
-  Row8 w[NC], dw[NC];
+  __shared__ __align__(16) float joined[NC * kMostWaves / 2 * kWave * N];
+  const int W = a.waves, threads = W * kWave;
+  const int mine = wave_in_block() / W, wave = wave_in_block() % W;  // its row of those at once
+  const int thread = wave * kWave + lane_id();
+  const int pieces = a.H / N;
+  Row<N> w[NC], dw[NC];
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
-    const int p = i * blockDim.x + threadIdx.x;
-    Piece<kWeightF32> piece;
+    const int p = i * threads + thread;
+    Piece<kWeightF32, N> piece;
     if (p < pieces) {
       piece.load(a.weight, p);
       w[i] = piece.get();
     }
 #pragma unroll
-    for (int j = 0; j < kPiece; ++j) dw[i].v[j] = 0.0f;
+    for (int j = 0; j < N; ++j) dw[i].v[j] = 0.0f;
   }
   int turn = 0;
-  for (int row = blockIdx.x; row < a.T; row += gridDim.x, turn ^= 1) {
+  for (int row0 = blockIdx.x * a.at_once; row0 < a.T; row0 += gridDim.x * a.at_once, turn ^= 1) {
+    const int row = row0 + mine;
+    const bool live = row < a.T;
     const int64_t at0 = int64_t(row) * pieces;
-    Piece<false> d[NC];
-    Piece<kF32> h[NC], through[NC];
+    Piece<false, N> d[NC];
+    Piece<kF32, N> h[NC], through[NC];
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int p = i * blockDim.x + threadIdx.x;
-      if (p < pieces) {
+      const int p = i * threads + thread;
+      if (live && p < pieces) {
         d[i].load(a.d_out, at0 + p);
         h[i].load(a.h, at0 + p);
         if (a.d_sum) through[i].load(a.d_sum, at0 + p);
       }
     }
-    const float inv = a.inv[row];
+    const float inv = live ? a.inv[row] : 0.0f;
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int p = i * blockDim.x + threadIdx.x;
-      if (p < pieces) {
-        const Row8 dd = d[i].get(), hh = h[i].get();
+      const int p = i * threads + thread;
+      if (live && p < pieces) {
+        const Row<N> dd = d[i].get(), hh = h[i].get();
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) {
+        for (int j = 0; j < N; ++j) {
           const float unit = hh.v[j] * inv;
           dw[i].v[j] = fmaf(dd.v[j], unit, dw[i].v[j]);
           dot = fmaf(dd.v[j] * w[i].v[j], unit, dot);
         }
       }
     }
-    const float mean = join_sum(dot, part[turn], wave, waves) / float(a.H);
+    const float mean = join_sum(dot, part[turn] + mine * W, wave, W) / float(a.H);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int p = i * blockDim.x + threadIdx.x;
-      if (p < pieces) {
-        const Row8 dd = d[i].get(), hh = h[i].get();
-        Row8 r;
+      const int p = i * threads + thread;
+      if (live && p < pieces) {
+        const Row<N> dd = d[i].get(), hh = h[i].get();
+        Row<N> r;
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j)
+        for (int j = 0; j < N; ++j)
           r.v[j] = inv * (dd.v[j] * w[i].v[j] - hh.v[j] * inv * mean);
         if (a.d_sum) {
-          const Row8 t = through[i].get();
+          const Row<N> t = through[i].get();
 #pragma unroll
-          for (int j = 0; j < kPiece; ++j) r.v[j] += t.v[j];
+          for (int j = 0; j < N; ++j) r.v[j] += t.v[j];
         }
-        if (a.d_res) store_piece<kF32>(a.d_res, at0 + p, r);
-        if (a.d_x) store_piece<false>(a.d_x, at0 + p, r);
+        if (a.d_res) store_piece<kF32, kF32>(a.d_res, at0 + p, r);
+        if (a.d_x) store_piece<false, true>(a.d_x, at0 + p, r);
       }
     }
   }
-  if (a.part) {
+  if (!a.part) return;
+  for (int r = 1; r < a.at_once; ++r) {  // (at_once > 1: at most half the waves a row)
+    if (mine == r) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int p = i * threads + thread;
+        if (p < pieces) {
+          if (r > 1) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) dw[i].v[j] += joined[p * N + j];
+          }
+#pragma unroll
+          for (int j = 0; j < N; ++j) joined[p * N + j] = dw[i].v[j];
+        }
+      }
+    }
+    __syncthreads();
+  }
+  if (mine == 0) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int p = i * blockDim.x + threadIdx.x;
-      if (p < pieces) store_piece<true>(a.part, int64_t(blockIdx.x) * pieces + p, dw[i]);
+      const int p = i * threads + thread;
+      if (p < pieces) {
+        if (a.at_once > 1) {
+#pragma unroll
+          for (int j = 0; j < N; ++j) dw[i].v[j] += joined[p * N + j];
+        }
+        store_piece<true, false>(a.part, int64_t(blockIdx.x) * pieces + p, dw[i]);
+      }
     }
   }
 }
 
-// d_weight[c] = the sum of part[.][c]: 64 columns a workgroup, each wave a
-// sixteenth of the rows, joined in wave order in 64 bits.
+// d_weight[c] = the sum of part[.][c]: 32 columns a workgroup, each half wave
+// every 32nd row, joined in 64 bits in their order.
+constexpr int kJoinCols = kWave / 2;
 __global__ __launch_bounds__(kMostWaves * kWave) void norm_grad_join(const float* part, int groups,
                                                                      int H, float* d_weight) {
-  __shared__ double sums[kMostWaves][kWave];
-  const int lane = lane_id(), wave = wave_in_block();
-  const int c = blockIdx.x * kWave + lane;
+  __shared__ double sums[2 * kMostWaves][kJoinCols];
+  const int at = threadIdx.x / kJoinCols, col = threadIdx.x % kJoinCols;
+  const int c = blockIdx.x * kJoinCols + col;
   double total = 0.0;
   if (c < H) {
 #pragma unroll 8
-    for (int g = wave; g < groups; g += kMostWaves) total += double(part[int64_t(g) * H + c]);
+    for (int g = at; g < groups; g += 2 * kMostWaves) total += double(part[int64_t(g) * H + c]);
   }
-  sums[wave][lane] = total;
+  sums[at][col] = total;
   __syncthreads();
-  if (wave == 0 && c < H) {
-    for (int w = 1; w < kMostWaves; ++w) total += sums[w][lane];
+  if (at == 0 && c < H) {
+    for (int o = 1; o < 2 * kMostWaves; ++o) total += sums[o][col];
     d_weight[c] = float(total);
   }
 }
@@ -414,7 +501,8 @@ __global__ __launch_bounds__(kMostWaves * kWave) void quantise_rows(QuantArgs a)
   __shared__ uint32_t tops[2][kMostWaves];
   const int waves = kWide ? blockDim.x / kWave : 1, wave = kWide ? wave_in_block() : 0;
   const int thread = kWide ? threadIdx.x : lane_id(), threads = kWide ? blockDim.x : kWave;
-  const int pieces = a.H / kPiece;
+  constexpr int N = kPieceOf<false>;
+  const int pieces = a.H / N;
   const int64_t stride = kWide ? gridDim.x : int64_t(gridDim.x) * (blockDim.x / kWave);
   int64_t i = kWide ? blockIdx.x : int64_t(blockIdx.x) * (blockDim.x / kWave) + wave_in_block();
   for (int turn = 0; i < a.count; i += stride) {
@@ -423,7 +511,7 @@ __global__ __launch_bounds__(kMostWaves * kWave) void quantise_rows(QuantArgs a)
     if (row >= a.cap && thread == 0) flag_error(a.err, MOE_ERRBIT_EXPERT_CAP);
     if (row < 0 || row >= a.cap) continue;  // the same for all that share the row
     const int64_t at0 = row * pieces;
-    Piece<false> x[NC];
+    Piece<false, N> x[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int p = c * threads + thread;
@@ -434,9 +522,9 @@ __global__ __launch_bounds__(kMostWaves * kWave) void quantise_rows(QuantArgs a)
     for (int c = 0; c < NC; ++c) {
       const int p = c * threads + thread;
       if (p < pieces) {
-        const Row8 r = x[c].get();
+        const Row<N> r = x[c].get();
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) top = max(top, magnitude(r.v[j]));
+        for (int j = 0; j < N; ++j) top = max(top, magnitude(r.v[j]));
       }
     }
     const Int8Scale s(join_max(top, tops[turn], wave, waves));
@@ -444,7 +532,7 @@ __global__ __launch_bounds__(kMostWaves * kWave) void quantise_rows(QuantArgs a)
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int p = c * threads + thread;
-      if (p < pieces) reinterpret_cast<vec2*>(a.q)[at0 + p] = s.codes(x[c].get());
+      if (p < pieces) store_codes(a.q, at0 + p, s.codes(x[c].get()));
     }
     if (thread == 0) a.scale[row] = s.scale;
   }
@@ -468,7 +556,9 @@ void launch_norm(int each, dim3 grid, int threads, hipStream_t st, const NormArg
   switch (each) {
     case 1: norm_rows<kF32, kWeightF32, kFmt, 1><<<grid, threads, 0, st>>>(a); break;
     case 2: norm_rows<kF32, kWeightF32, kFmt, 2><<<grid, threads, 0, st>>>(a); break;
-    default: norm_rows<kF32, kWeightF32, kFmt, 4><<<grid, threads, 0, st>>>(a);
+    case 4: norm_rows<kF32, kWeightF32, kFmt, 4><<<grid, threads, 0, st>>>(a); break;
+    default:  // only a float32 stream has as many pieces
+      norm_rows<kF32, kWeightF32, kFmt, kF32 ? 8 : 4><<<grid, threads, 0, st>>>(a);
   }
 }
 
@@ -487,17 +577,25 @@ void launch_grad(int each, dim3 grid, int threads, hipStream_t st, const NormGra
   switch (each) {
     case 1: norm_grad<kF32, kWeightF32, 1><<<grid, threads, 0, st>>>(a); break;
     case 2: norm_grad<kF32, kWeightF32, 2><<<grid, threads, 0, st>>>(a); break;
-    default: norm_grad<kF32, kWeightF32, 4><<<grid, threads, 0, st>>>(a);
+    case 4: norm_grad<kF32, kWeightF32, 4><<<grid, threads, 0, st>>>(a); break;
+    default:  // only a float32 stream has as many pieces
+      norm_grad<kF32, kWeightF32, kF32 ? 8 : 4><<<grid, threads, 0, st>>>(a);
   }
 }
 
 template <bool kWide>
 void launch_quant(int each, dim3 grid, int threads, hipStream_t st, const QuantArgs& a) {
-  switch (each) {
-    case 1: quantise_rows<kWide, 1><<<grid, threads, 0, st>>>(a); break;
-    case 2: quantise_rows<kWide, 2><<<grid, threads, 0, st>>>(a); break;
-    case 4: quantise_rows<kWide, 4><<<grid, threads, 0, st>>>(a); break;
-    default: quantise_rows<kWide, 8><<<grid, threads, 0, st>>>(a);
+  if constexpr (kWide) {
+    if (each == 4)
+      quantise_rows<true, 4><<<grid, threads, 0, st>>>(a);
+    else
+      quantise_rows<true, 8><<<grid, threads, 0, st>>>(a);
+  } else {
+    switch (each) {
+      case 1: quantise_rows<false, 1><<<grid, threads, 0, st>>>(a); break;
+      case 2: quantise_rows<false, 2><<<grid, threads, 0, st>>>(a); break;
+      default: quantise_rows<false, 4><<<grid, threads, 0, st>>>(a);
+    }
   }
 }
 
@@ -507,9 +605,8 @@ bool norm_shape_ok(const moe_shape_t* s, int stream_type, int weight_type) {
          (weight_type == MOE_TYPE_F32 || weight_type == MOE_TYPE_BF16);
 }
 
-// Workgroups of the gradient: as many as are resident at once (two of each CU),
-// each with a row at least.
-int grad_groups(int T) { return std::min(T, 512); }
+// Workgroups of the gradient, at most: two for each CU, all resident at once.
+constexpr int kGradGroups = 512;
 
 }  // namespace
 
@@ -530,12 +627,14 @@ int moe_norm(const moe_shape_t* shape, int stream_type, const uint16_t* x, const
   if ((residual == nullptr) != (sum == nullptr)) return MOE_ERR_ARG;
   if ((format != 0) != (q != nullptr) || (format != 0) != (q_scale != nullptr)) return MOE_ERR_ARG;
   const NormArgs a{x, residual, weight, sum, out, q, q_scale, inv_rms, eps, shape->T, shape->H};
-  const int pieces = shape->H / kPiece;
-  const int each = pieces_a_lane(pieces), threads = waves_for(pieces, each) * kWave;
+  const bool f32 = stream_type == MOE_TYPE_F32;
+  const int pieces = shape->H / (f32 ? kPieceOf<true> : kPieceOf<false>);
+  const int each = pieces_a_lane(pieces);
+  const int threads = waves_for(pieces, each) * kWave;
   const dim3 grid(std::min(shape->T, kMostGroups));
   const int fmt = format == 0 ? kNone : format == MOE_ROWS_INT8 ? kInt8 : kMxfp8;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (stream_type == MOE_TYPE_F32) {
+  if (f32) {
     if (weight_type == MOE_TYPE_F32)
       launch_norm<true, true>(fmt, each, grid, threads, st, a);
     else
@@ -551,7 +650,7 @@ int moe_norm(const moe_shape_t* shape, int stream_type, const uint16_t* x, const
 
 size_t moe_norm_workspace_bytes(const moe_shape_t* shape) {
   if (!norm_shape_ok(shape, MOE_TYPE_F32, MOE_TYPE_F32)) return 0;
-  return size_t(grad_groups(shape->T)) * shape->H * sizeof(float);
+  return size_t(std::min(shape->T, kGradGroups)) * shape->H * sizeof(float);
 }
 
 int moe_norm_backward(const moe_shape_t* shape, int stream_type, const uint16_t* d_out,
@@ -570,15 +669,24 @@ int moe_norm_backward(const moe_shape_t* shape, int stream_type, const uint16_t*
   if (!rows && !d_weight) return MOE_OK;
   if (!d_x && !d_residual && !d_weight) return MOE_ERR_ARG;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const int groups = grad_groups(shape->T);
   float* part = d_weight ? static_cast<float*>(workspace) : nullptr;
+  int groups = 0;
   if (rows) {
-    const NormGradArgs a{d_out, sum,        weight, d_sum,    inv_rms,
-                         d_x,   d_residual, part,   shape->T, shape->H};
-    const int pieces = shape->H / kPiece;
-    const int each = pieces_a_lane(pieces), threads = waves_for(pieces, each) * kWave;
+    const bool f32 = stream_type == MOE_TYPE_F32;
+    const int pieces = shape->H / (f32 ? kPieceOf<true> : kPieceOf<false>);
+    // Two pieces a lane halve the waves a row, so that twice as many rows meet before
+    // they reach memory: where every workgroup has one row, 509 x 5,120 in bf16 11.3
+    // us against 13.6, 512 x 7,168 in float32 17.7 against 19.2; with 1,024 rows 17.8
+    // against 16.0, with 64 7.9 against 6.8.
+    const int each = std::max(shape->T > 128 && shape->T <= kGradGroups ? (f32 ? 4 : 2) : 1,
+                              pieces_a_lane(pieces));
+    const int waves = waves_for(pieces, each), at_once = kMostWaves / waves;
+    const int threads = waves * at_once * kWave;
+    groups = std::min((shape->T + at_once - 1) / at_once, kGradGroups);
+    const NormGradArgs a{d_out,      sum,  weight,   d_sum,    inv_rms, d_x,
+                         d_residual, part, shape->T, shape->H, waves,   at_once};
     const dim3 grid(groups);
-    if (stream_type == MOE_TYPE_F32) {
+    if (f32) {
       if (weight_type == MOE_TYPE_F32)
         launch_grad<true, true>(each, grid, threads, st, a);
       else
@@ -592,8 +700,8 @@ int moe_norm_backward(const moe_shape_t* shape, int stream_type, const uint16_t*
     const int status = launch_status();
     if (status != MOE_OK || !d_weight) return status;
   }
-  norm_grad_join<<<(shape->H + kWave - 1) / kWave, kMostWaves * kWave, 0, st>>>(part, groups,
-                                                                                shape->H, d_weight);
+  norm_grad_join<<<(shape->H + kJoinCols - 1) / kJoinCols, kMostWaves * kWave, 0, st>>>(
+      part, groups, shape->H, d_weight);
   return launch_status();
 }
 
@@ -608,14 +716,18 @@ int moe_quantise_rows(const moe_shape_t* shape, const uint16_t* rows, const int3
   if (count == 0) return MOE_OK;
   if (cap_expert > 0 && (!rows || !q || !scale)) return MOE_ERR_ARG;
   const QuantArgs a{rows, pair_row, q, scale, err_word, cap_expert, count, shape->H};
-  const int pieces = shape->H / kPiece;
+  const int pieces = shape->H / kPieceOf<false>;
   hipStream_t st = static_cast<hipStream_t>(stream);
+  // A wave takes rows of up to 2,048 values alone; longer ones four pieces a lane,
+  // few waves that wait for each other (16,384 rows of 5,120: one piece a lane 84
+  // us, two 58, four 50, eight 52).
   if (pieces <= 4 * kWave) {
     const int64_t groups = (count + 3) / 4;
-    launch_quant<false>(pieces <= kWave ? 1 : pieces <= 2 * kWave ? 2 : 4,
-                        dim3(uint32_t(std::min<int64_t>(groups, kMostGroups))), 4 * kWave, st, a);
+    const int each = pieces <= kWave ? 1 : pieces <= 2 * kWave ? 2 : 4;
+    launch_quant<false>(each, dim3(uint32_t(std::min<int64_t>(groups, kMostGroups))), 4 * kWave, st,
+                        a);
   } else {
-    const int each = pieces_a_lane(pieces);
+    const int each = std::max(4, pieces_a_lane(pieces));
     launch_quant<true>(each, dim3(uint32_t(std::min<int64_t>(count, kMostGroups))),
                        waves_for(pieces, each) * kWave, st, a);
   }
