@@ -491,19 +491,20 @@ struct Form {
   int fixed1, step1, fixed2, step2;
 };
 
-// The times are fitted to 500 measured ones: rows from 1 to 8,192, plain and of 2 to
-// 48 experts, K from 1,024 to 7,168, N from 1,024 to 7,168. Chosen by them, a launch
-// takes 1.5% more than in the form that was the fastest there, 25% at most. Every
-// form is the best of some sizes by 20% and more (K = 5,120, N = 4,096 with SwiGLU: 24
-// rows 6.8 us in form 0 and 7.9 in the next; 64 rows 8.2 in form 1, 11.1 in form 2, 18.4 in form
-// 4; 128 rows 11.2 in form 2, 13.8 and 14.8 around it; 256 rows 15.2 in form 3, 19.2 and 19.0
-// around it; 512 rows 20.0 in form 4, 35.6 in the next; 1,300 rows 40.8 in form 5, 45.8 and 59.3
-// around it; 4,093 rows 83 in form 6, 93 in form 5).
+// The times are fitted to 790 measured ones: rows from 1 to 16,384, plain and of 2 to
+// 48 experts, K and N from 1,024 to 7,168. Chosen by them, a launch takes 0.6% more than
+// in the form that was the fastest there, 31% at most (20 rows each of 2 experts). Every
+// form is the best of some sizes (K = 5,120, N = 4,096 with SwiGLU, kernel us, the forms
+// next to it in brackets): 32 rows 7.1 in form 0 (8.4); 64 rows 8.2 in form 1 (11.2, 11.2);
+// 128 rows 11.1 in form 2 (13.6, 14.7); 256 rows 15.1 in form 3 (19.2, 18.9); 512 rows 19.5
+// in form 4 (21.0, 32.7); 1,300 rows 38.9 in form 5 (45.0, 59.9); 4,093 rows 78.9 in form 6
+// (87.5). Tiles of 128 x 128 by 4 waves were 3% better than form 5 at 2,048 rows of K =
+// 2,048 and 10% worse for experts: there is no form of them.
 constexpr Form kForms[] = {
-    {32, 16, 8, 8, 1, 1470, 530, 0, 0},        {32, 32, 4, 4, 1, 1840, 400, 0, 0},
-    {64, 32, 4, 4, 1, 2640, 615, 0, 0},        {64, 64, 2, 1, 2, 3240, 220, 2590, 460},
-    {64, 128, 4, 1, 2, 2330, 325, 3690, 680},  {128, 128, 4, 1, 2, 2650, 735, 5060, 1000},
-    {256, 256, 8, 1, 1, 10230, 1200, 0, 0},
+    {32, 16, 8, 8, 1, 1770, 490, 0, 0},       {32, 32, 4, 4, 1, 1900, 386, 0, 0},
+    {64, 32, 4, 4, 1, 2510, 564, 0, 0},       {64, 64, 2, 1, 2, 3520, 223, 2970, 435},
+    {64, 128, 4, 1, 2, 2300, 330, 3410, 690}, {128, 256, 8, 1, 1, 5770, 782, 0, 0},
+    {256, 256, 8, 1, 1, 9700, 1296, 0, 0},
 };
 constexpr int kFormCount = sizeof(kForms) / sizeof(kForms[0]);
 
@@ -516,7 +517,7 @@ void launch(int form, dim3 grid, hipStream_t st, const Int8Args& a) {
     case 2: product_few<kSwiglu, 4, 2, 4, 3><<<grid, threads, 0, st>>>(a); break;
     case 3: product_tile<kSwiglu, 64, 64, 2, 1, 4, 2><<<grid, threads, 0, st>>>(a); break;
     case 4: product_tile<kSwiglu, 64, 128, 2, 2, 3, 2><<<grid, threads, 0, st>>>(a); break;
-    case 5: product_tile<kSwiglu, 128, 128, 2, 2, 2, 1><<<grid, threads, 0, st>>>(a); break;
+    case 5: product_tile<kSwiglu, 128, 256, 2, 4, 3, 1><<<grid, threads, 0, st>>>(a); break;
     default: product_tile<kSwiglu, 256, 256, 2, 4, 2, 1><<<grid, threads, 0, st>>>(a);
   }
 }

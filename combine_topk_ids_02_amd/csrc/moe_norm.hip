@@ -196,9 +196,21 @@ struct Int8Scale {
 #pragma unroll
       for (int i = 0; i < N; ++i) r.v[i] *= move;
     }
+    // The product plus 1.5 * 2^23 has the nearest whole number in its low bits (as
+    // ties to even; the two must not become one fma), the code in its low byte.
+    uint32_t b[N];
+    {
+#pragma clang fp contract(off)
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      q.w[i / 4] |= uint32_t(int(__builtin_rintf(r.v[i] * factor)) & 0xFF) << (i % 4 * 8);
+      for (int i = 0; i < N; ++i) b[i] = __float_as_uint(r.v[i] * factor + 0x1.8p23f);
+    }
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint32_t* p = b + 4 * i;
+      const uint32_t lo = __builtin_amdgcn_perm(p[1], p[0], 0x0C0C0400u);
+      const uint32_t hi = __builtin_amdgcn_perm(p[3], p[2], 0x0C0C0400u);
+      q.w[i] = lo | hi << 16;
+    }
     return q;
   }
 };
@@ -629,7 +641,10 @@ int moe_norm(const moe_shape_t* shape, int stream_type, const uint16_t* x, const
   const NormArgs a{x, residual, weight, sum, out, q, q_scale, inv_rms, eps, shape->T, shape->H};
   const bool f32 = stream_type == MOE_TYPE_F32;
   const int pieces = shape->H / (f32 ? kPieceOf<true> : kPieceOf<false>);
-  const int each = pieces_a_lane(pieces);
+  // The maximum of 8-bit rows is a second wait for the whole row: two pieces a lane,
+  // and more rows at once on a CU (4,093 x 7,168 39 us against 49, 64 x 5,120 4.4 against 4.1).
+  const int each = std::max(format == MOE_ROWS_INT8 && shape->T > 256 ? 2 : 1,
+                            pieces_a_lane(pieces));
   const int threads = waves_for(pieces, each) * kWave;
   const dim3 grid(std::min(shape->T, kMostGroups));
   const int fmt = format == 0 ? kNone : format == MOE_ROWS_INT8 ? kInt8 : kMxfp8;
