@@ -539,10 +539,13 @@ int64_t time_of(const Form& f, int64_t pairs, int64_t active, int N, int K) {
 }
 
 int form_of(int64_t pairs, int64_t active, int N, int K) {
-  int best = 0;
-  for (int f = 1; f < kFormCount; ++f)
+  int best = 1;
+  for (int f = 0; f < kFormCount; ++f) {
+    // form 0 reaches from a gate to its other factor by a 32-bit offset
+    if (f == 0 && int64_t(N) * K >= int64_t(1) << 31) continue;
     if (time_of(kForms[f], pairs, active, N, K) < time_of(kForms[best], pairs, active, N, K))
       best = f;
+  }
   return best;
 }
 

@@ -249,6 +249,23 @@ def test_weights_far_into_their_tensor():
     assert bool((out[:-3] == 0).all())
 
 
+def test_gates_far_from_their_other_factors():
+    """Gates and other factors more than 2^31 bytes apart."""
+    N, K = 1 << 17, 32768
+    half = N // 2
+    g = gen(11)
+    w = torch.zeros(1, N, K, dtype=torch.int8, device="cuda")
+    w[0, half - 50:half], w[0, N - 50:] = codes(g, 50, K), codes(g, 50, K)
+    ws = torch.full((1, N), 2.0 ** -8, device="cuda")
+    pick = torch.cat([torch.arange(half - 50, half), torch.arange(N - 50, N)]).cuda()
+    for rows in (1, 20, 60, 200, 1000):
+        say(f"far gates rows={rows}")
+        q, xs = codes(g, rows, K), torch.full((rows,), 2.0 ** -9, device="cuda")
+        out, _ = run(q, xs, w, ws, "swiglu")
+        check(q, xs, w[0, pick], ws[0, pick], "swiglu", out[:, -50:].view(torch.bfloat16))
+        assert bool((out[:, :-50] == 0).all())
+
+
 def test_two_streams_at_once_and_a_graph():
     """Calls on two streams at once, and a captured one replayed with new rows,
     give what each gives alone."""
