@@ -16,6 +16,11 @@ from dataclasses import dataclass
 
 import torch  # loads the HIP runtime the library binds to; must come first
 
+try:  # the costly part of a small call in C++ (csrc/binding.cpp); without it: slower
+    from . import _binding as _fast
+except ImportError:
+    _fast = None
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_dispatch.so")
 
@@ -71,6 +76,9 @@ class MoeError(RuntimeError):
 
 
 _lib = None
+_address = None if _fast is None else _fast.address
+# its functions, in the order of its bind()
+_FAST_CALLS = ("moe_norm", "moe_norm_backward", "moe_quantise_rows", "moe_int8_product")
 
 
 def lib():
@@ -163,8 +171,17 @@ def lib():
     if L.moe_abi_version() != ABI_VERSION:
         raise MoeError(f"{LIB_PATH} has ABI version {L.moe_abi_version()}, this binding "
                        f"expects {ABI_VERSION}: rebuild with __graft_entry__.build()")
+    if _fast is not None:
+        _fast.bind(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value
+                     for name in _FAST_CALLS))
     _lib = L
     return L
+
+
+def _entry(name: str):
+    """A function of the library, through the C++ module where it is there."""
+    L = lib()
+    return getattr(L if _fast is None else _fast, name)
 
 
 def _check(status: int, what: str) -> None:
@@ -644,6 +661,10 @@ def _dev(t: torch.Tensor | None, name: str, dtype, shape: tuple, device) -> int 
     on `device`; None for None. Raises MoeError."""
     if t is None:
         return None
+    if _address is not None:
+        at = _address(t, dtype, device.index, shape)
+        if at is not None:
+            return at  # else what is wrong is found below
     if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
         return t.data_ptr()
     if t.dtype != dtype:
@@ -840,7 +861,7 @@ def norm(x: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6, residual=N
     stream = bf16 if residual is None else residual.dtype
     code = 1 if residual is None else _norm_type(residual, "residual")
     kind, scales = (torch.int8, (T,)) if fmt == "int8" else (torch.uint8, (T, H // 32))
-    _call(lib().moe_norm, "moe_norm", dev, _sizes(T, H, 1, 1), code,
+    _call(_entry("moe_norm"), "moe_norm", dev, _sizes(T, H, 1, 1), code,
           _dev(x, "x", x.dtype, (T, H), dev), _dev(residual, "residual", stream, (T, H), dev),
           _dev(sum, "sum", stream, (T, H), dev), _norm_type(weight, "weight"),
           _dev(weight, "weight", weight.dtype, (H,), dev), eps,
@@ -877,7 +898,7 @@ def norm_backward(d_out: torch.Tensor, sum: torch.Tensor, inv_rms, weight, *, d_
     T, H = d_out.shape
     code, stream, f32 = _norm_type(sum, "sum"), sum.dtype, torch.float32
     room = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _call(lib().moe_norm_backward, "moe_norm_backward", dev, _sizes(T, H, 1, 1), code,
+    _call(_entry("moe_norm_backward"), "moe_norm_backward", dev, _sizes(T, H, 1, 1), code,
           _dev(d_out, "d_out", d_out.dtype, (T, H), dev), _dev(sum, "sum", stream, (T, H), dev),
           _dev(inv_rms, "inv_rms", f32, (T,), dev), _norm_type(weight, "weight"),
           _dev(weight, "weight", weight.dtype, (H,), dev),
@@ -905,7 +926,7 @@ def quantise_rows(rows: torch.Tensor, q, scale, *, pair_row=None, err=None) -> N
         if pair_row.dim() != 2:
             raise MoeError(f"pair_row has shape {tuple(pair_row.shape)}, the call needs [T, k]")
         T, k = pair_row.shape
-    _call(lib().moe_quantise_rows, "moe_quantise_rows", dev, _sizes(T, H, k, k),
+    _call(_entry("moe_quantise_rows"), "moe_quantise_rows", dev, _sizes(T, H, k, k),
           _dev(rows, "rows", rows.dtype, (cap, H), dev),
           _dev(pair_row, "pair_row", torch.int32, (T, k), dev), cap,
           _dev(q, "q", torch.int8, (cap, H), dev),
@@ -939,7 +960,7 @@ def int8_product(rows: torch.Tensor, row_scale, w_q, w_scale, out, *, act: str |
         T = cap // k
     if out.dtype not in ROW_TYPES:
         raise MoeError(f"out must be bf16 (or its bits), got {out.dtype}")
-    _call(lib().moe_int8_product, "moe_int8_product", dev, _sizes(T, H, E, k), N, code,
+    _call(_entry("moe_int8_product"), "moe_int8_product", dev, _sizes(T, H, E, k), N, code,
           _dev(rows, "rows", i8, (cap, H), dev), _dev(row_scale, "row_scale", f32, (cap,), dev),
           _dev(expert_counts, "expert_counts", i32, (E,), dev),
           _dev(expert_offsets, "expert_offsets", i32, (E + 1,), dev), cap,

@@ -51,3 +51,30 @@ def test_binding():
         moe.int8_product(q, s, w, ws, out)
     with pytest.raises(moe.MoeError, match="activation"):
         moe.int8_product(q, s, w, ws, out, act="gelu")
+
+
+def test_the_bindings_cpp_part():
+    """It says no to what is not a GPU's tensor, and passes numbers and structures on
+    as ctypes does."""
+    if moe._fast is None:
+        pytest.skip("not built, or built after the package was imported")
+    t = torch.zeros(4, 64)
+    for args in ((t, torch.float32, 0, (4, 64)), (t, torch.float32, None, (4, 64)),
+                 (None, torch.float32, 0, (4, 64)), (t, torch.float32, 0), (3, 4, 5, 6)):
+        assert moe._fast.address(*args) is None
+    moe.lib()
+    shape = moe.MoeShape(0, 64, 1, 1, 1)
+    args = [shape, 1, 0x10000, None, None, 0, 0x10000, 1e-6, 0x10000, 0, None, None, None, None]
+    assert moe._fast.moe_norm(*args) == moe.MOE_OK == moe.lib().moe_norm(*args)
+    for at, bad in ((7, 0.0), (1, 2), (2, 0x10008), (9, 3)):
+        wrong = list(args)
+        wrong[at] = bad
+        assert moe._fast.moe_norm(*wrong) == moe.MOE_ERR_ARG == moe.lib().moe_norm(*wrong)
+    for wrong in (args[:-1], args + [None]):
+        with pytest.raises(TypeError):
+            moe._fast.moe_norm(*wrong)
+    for at, bad in ((1, 1 << 40), (1, "1"), (2, 1.5), (7, "x"), (0, object())):
+        wrong = list(args)
+        wrong[at] = bad
+        with pytest.raises((TypeError, OverflowError, BufferError)):
+            moe._fast.moe_norm(*wrong)

@@ -260,7 +260,12 @@ def test_training_step_of_two_norms():
         assert abs(slope - float(dw2[c])) <= 2 * HALF * terms
 
 
-def test_binding_refuses_wrong_tensors():
+@pytest.mark.parametrize("fast", [True, False])
+def test_binding_refuses_wrong_tensors(fast, monkeypatch):
+    """With the binding's C++ part and without it."""
+    if not fast:
+        monkeypatch.setattr(moe, "_fast", None)
+        monkeypatch.setattr(moe, "_address", None)
     dev = "cuda"
     x, w = torch.zeros(4, 64, dtype=BF, device=dev), torch.zeros(64, device=dev)
     f = torch.zeros(4, 64, device=dev)
@@ -303,3 +308,13 @@ def test_binding_refuses_wrong_tensors():
         with pytest.raises(moe.MoeError):
             call()
             print("accepted:", n)
+    g = torch.Generator(device=dev)
+    g.manual_seed(3)
+    x.copy_(torch.randn(4, 64, device=dev, generator=g))
+    w += 1
+    moe.norm(x, w, fmt="int8", q=q, q_scale=s, inv_rms=inv)
+    wsc += 1
+    wq += 1
+    moe.int8_product(q, s, wq, wsc, out)
+    want = (q.float().sum(dim=1) * s).to(BF)
+    assert torch.equal(out, want[:, None].expand(4, 32))
