@@ -941,8 +941,8 @@ def int8_product(rows: torch.Tensor, row_scale, w_q, w_scale, out, *, act: str |
     or [cap, N / 2] with act "swiglu". With expert_counts [E] and expert_offsets
     [E + 1] (the layout's, or those of a slice of its experts, as for
     expert_product()) the rows are the expert-grouped buffer's, and T * k of them
-    are in use as far as the host knows; without, all rows (or the first T * k)
-    have the one expert."""
+    are in use as far as the host knows; without, the first T * k rows have the one
+    expert. Without T it is all rows."""
     if act not in ACTS:
         raise MoeError(f"unknown activation {act!r}: one of {sorted(a for a in ACTS if a)}")
     dev = rows.device
@@ -957,7 +957,7 @@ def int8_product(rows: torch.Tensor, row_scale, w_q, w_scale, out, *, act: str |
     code = ACTS[act]
     i8, i32, f32 = torch.int8, torch.int32, torch.float32
     if T is None:
-        T = cap // k
+        T, k = cap, 1
     if out.dtype not in ROW_TYPES:
         raise MoeError(f"out must be bf16 (or its bits), got {out.dtype}")
     _call(_entry("moe_int8_product"), "moe_int8_product", dev, _sizes(T, H, E, k), N, code,

@@ -526,16 +526,16 @@ int64_t column_tiles(const Form& f, int N) { return (N + f.weights - 1) / f.weig
 
 // The time of a form in ns, for `pairs` rows of `active` experts; an expert's last
 // chunk is half full on average.
-int64_t time_of(const Form& f, int64_t pairs, int64_t active, int N, int K) {
+double time_of(const Form& f, int64_t pairs, int64_t active, int N, int K) {
   const int64_t chunks = active == 1 ? (pairs + f.rows - 1) / f.rows
                                      : std::max(active, pairs / f.rows + active / 2);
   const int64_t granules = (K + kGranule - 1) / kGranule;
   const int64_t steps = (granules + f.over_k - 1) / f.over_k;
   const int64_t tiles = chunks * column_tiles(f, N), round = int64_t(256) * f.per_cu;
   const int64_t full = tiles / round, rest = tiles % round;
-  const int64_t one = f.fixed1 + f.step1 * steps, two = f.fixed2 + f.step2 * steps;
-  if (f.per_cu == 1) return (full + (rest > 0)) * one;
-  return full * two + (rest > 256 ? two : rest > 0 ? one : 0);
+  const double one = f.fixed1 + f.step1 * double(steps), two = f.fixed2 + f.step2 * double(steps);
+  if (f.per_cu == 1) return double(full + (rest > 0)) * one;
+  return double(full) * two + (rest > 256 ? two : rest > 0 ? one : 0.0);
 }
 
 int form_of(int64_t pairs, int64_t active, int N, int K) {

@@ -179,6 +179,20 @@ def test_counts_of_no_layout(T):
         run(q, xs, w, ws, None, counts, off, T, 1)
 
 
+def test_numbers_of_rows_that_the_binding_is_given():
+    """Without T all rows, whatever k; with T the first T * k."""
+    q, xs, w, ws = inputs(12, 7, 1, 32, 64)
+    whole, _ = run(q, xs, w, ws, None)
+    out, _ = run(q, xs, w, ws, None, k=2)
+    assert torch.equal(out, whole)
+    out, _ = run(q, xs, w, ws, None, T=2, k=3)
+    assert torch.equal(out[:6], whole[:6]) and bool((out[6:] == 0x5A5A).all())
+    counts = np.array([3, 4])
+    w2, ws2 = w.repeat(2, 1, 1), ws.repeat(2, 1)
+    out, _ = run(q, xs, w2, ws2, None, counts, layout(counts, 1, 0), k=4)
+    assert torch.equal(out, whole)
+
+
 def test_a_slice_of_the_experts():
     counts = np.array([4, 9, 0, 33, 2, 80])
     off = layout(counts, 16, 0)
