@@ -23,6 +23,7 @@ using namespace moe;
 
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
@@ -118,13 +119,13 @@ struct Chunks {
 // XCDs one by one, so each XCD is given a contiguous eighth of the order, and
 // the order goes through the columns of 8 chunks at a time: what an XCD works on
 // at one time shares rows and weights in its L2.
-__device__ __forceinline__ void place_of(int64_t i, int total, int tiles, int* chunk, int* col) {
-  const int64_t all = int64_t(total) * tiles, each = all / 8, more = all % 8;
-  const int64_t x = i % 8, at = x * each + min(x, more) + i / 8;
-  const int64_t per = int64_t(8) * tiles;
-  const int64_t g = at / per, rest = at - g * per;
-  const int held = min(8, total - int(g) * 8);
-  *chunk = int(g) * 8 + int(rest % held);
+template <typename T>
+__device__ __forceinline__ void place_of(T i, T total, T tiles, int* chunk, int* col) {
+  const T all = total * tiles, x = i % 8;
+  const T at = x * (all / 8) + min(x, T(all % 8)) + i / 8;
+  const T g = at / (8 * tiles), rest = at - g * 8 * tiles;
+  const T held = min(T(8), T(total - g * 8));
+  *chunk = int(g * 8 + rest % held);
   *col = int(rest / held);
 }
 
@@ -153,7 +154,11 @@ __global__ __launch_bounds__(W * kWave) void product_few(Int8Args a) {
   constexpr int L = 2 * (NT + MT);         // loads of a granule, 8 rows each
   constexpr int kStage = L * 8 * kGranule;
   constexpr int kJoin = W * NT * MT * 4 * kWave * 4;
-  __shared__ __align__(16) char lds[W * S * kStage > kJoin ? W * S * kStage : kJoin];
+  constexpr int kRoom = W * S * kStage > kJoin ? W * S * kStage : kJoin;
+  // One array for all of LDS: with two the compiler waits for every load that is on
+  // its way to LDS before each read of it.
+  __shared__ __align__(16) char lds[kRoom + (16 * NT + BM) * 4];
+  float* scales = reinterpret_cast<float*>(lds + kRoom);  // of the weight rows, then the rows
   int(*part)[NT * MT * 4][kWave] = reinterpret_cast<int(*)[NT * MT * 4][kWave]>(lds);
   const int lane = lane_id(), wave = wave_in_block();
   const int m = lane & 15, kq = lane >> 4;
@@ -167,7 +172,10 @@ __global__ __launch_bounds__(W * kWave) void product_few(Int8Args a) {
   for (int64_t i = blockIdx.x; i < all; i += gridDim.x) {
     int chunk, col, e, nr;
     int64_t row0;
-    place_of(i, chunks.total, a.tiles, &chunk, &col);
+    if (all < int64_t(1) << 28)  // divisions in 32 bits, where they do
+      place_of<uint32_t>(i, chunks.total, a.tiles, &chunk, &col);
+    else
+      place_of<int64_t>(i, chunks.total, a.tiles, &chunk, &col);
     if (!chunks.get(chunk, &e, &row0, &nr)) return;
     const int n0 = col * kCols;
     const int8_t* w0 = a.w + (int64_t(e) * a.N + n0) * a.K;
@@ -181,6 +189,15 @@ __global__ __launch_bounds__(W * kWave) void product_few(Int8Args a) {
                             max(0, min(16, limit - (kSwiglu ? n0 : n0 + 16 * h))) * a.K);
     }
     const buffer xb = make_buffer(a.rows + row0 * a.K, nr * a.K);
+    // The scales come first, so that no one waits for them at the end.
+    float scale = 0.0f;
+    if (threadIdx.x < 16 * NT + BM) {
+      const int r = threadIdx.x, c = kMixed ? r % 8 : kSwiglu ? r % 16 : r;
+      if (r >= 16 * NT)
+        scale = r - 16 * NT < nr ? a.row_scale[row0 + r - 16 * NT] : 0.0f;
+      else if (n0 + c < limit)
+        scale = a.w_scale[int64_t(e) * a.N + n0 + c + (r == c ? 0 : half)];
+    }
 
     // Load j fills rows 8 j .. 8 j + 7 of a granule: the weights' tiles, then the
     // rows'; a lane 16 bytes, lane l the slot l % 8 of row l / 8. Slot s of row r
@@ -207,6 +224,7 @@ __global__ __launch_bounds__(W * kWave) void product_few(Int8Args a) {
 #pragma unroll
     for (int s = 0; s < S - 1; ++s)
       if (s < steps) load(s, s);
+    if (threadIdx.x < 16 * NT + BM) scales[threadIdx.x] = scale;
     int slot = 0;
     for (int s = 0; s < steps; ++s) {
       // this granule has come when at most the later ones are on their way, and
@@ -267,15 +285,16 @@ __global__ __launch_bounds__(W * kWave) void product_few(Int8Args a) {
         for (int o = 0; o < W; ++o) v += part[o][(h * MT + q) * 4 + r][l];
         return float(v);
       };
-      const float xs = row < nr ? a.row_scale[row0 + row] : 0.0f;
-      const float* ws = a.w_scale + int64_t(e) * a.N;
+      const float xs = scales[16 * NT + row];
       __bf16* to = reinterpret_cast<__bf16*>(a.out) + (row0 + row) * a.wide;
 #pragma unroll
       for (int h = 0; h < (kSwiglu ? 1 : NT); ++h) {
         const int n = n0 + 16 * h + 4 * kq + r;
         if (row >= nr || n >= limit || (kMixed && kq >= 2)) continue;
-        float y = sum(h, lane) * xs * ws[n];
-        if (kSwiglu) y = swiglu(y, sum(NT - 1, kMixed ? lane + 32 : lane) * xs * ws[half + n]);
+        const float* ws = scales + 16 * h + 4 * kq + r;
+        float y = sum(h, lane) * xs * ws[0];
+        if (kSwiglu)
+          y = swiglu(y, sum(NT - 1, kMixed ? lane + 32 : lane) * xs * ws[kMixed ? 8 : 16]);
         to[n] = __bf16(y);
       }
     }
@@ -302,7 +321,10 @@ __global__ __launch_bounds__(WM * WN * kWave) void product_tile(Int8Args a) {
   // then lie in different banks
   constexpr int kPitch = kCols * 2 + 16;
   constexpr int kRoom = S * kStage > BM * kPitch ? S * kStage : BM * kPitch;
-  __shared__ __align__(16) char lds[kRoom];
+  // One array for all of LDS: with two the compiler waits for every load that is on
+  // its way to LDS before each read of it (512 rows, K = 5,120, N = 4,096: 33 us, not 20).
+  __shared__ __align__(16) char lds[kRoom + (BN + BM) * 4];
+  float* scales = reinterpret_cast<float*>(lds + kRoom);  // of the weight rows, then the rows
   const int lane = lane_id(), wave = wave_in_block();
   const int wm = wave / WN, wn = wave % WN;
   const int half = a.N / 2, limit = kSwiglu ? half : a.N;
@@ -312,13 +334,32 @@ __global__ __launch_bounds__(WM * WN * kWave) void product_tile(Int8Args a) {
   for (int64_t i = blockIdx.x; i < all; i += gridDim.x) {
     int chunk, col, e, nr;
     int64_t row0;
-    place_of(i, chunks.total, a.tiles, &chunk, &col);
+    if (all < int64_t(1) << 28)  // divisions in 32 bits, where they do
+      place_of<uint32_t>(i, chunks.total, a.tiles, &chunk, &col);
+    else
+      place_of<int64_t>(i, chunks.total, a.tiles, &chunk, &col);
     if (!chunks.get(chunk, &e, &row0, &nr)) return;
     const int n0 = col * kCols, held = min(kCols, limit - n0);
     const int8_t* w0 = a.w + (int64_t(e) * a.N + n0) * a.K;
     const buffer wg = make_buffer(w0, held * a.K);
     const buffer wu = make_buffer(w0 + int64_t(kSwiglu ? half : 0) * a.K, held * a.K);
     const buffer xb = make_buffer(a.rows + row0 * a.K, nr * a.K);
+
+    // The scales come first, so that no one waits for them at the end: one of each
+    // thread, or two.
+    constexpr int kScales = (BN + BM + W * kWave - 1) / (W * kWave);
+    float scale[kScales];
+#pragma unroll
+    for (int k = 0; k < kScales; ++k) {
+      const int r = k * W * kWave + threadIdx.x, c = kSwiglu ? r / 64 * 32 + r % 32 : r;
+      scale[k] = 0.0f;
+      if (r < BN) {
+        if (c < held)
+          scale[k] = a.w_scale[int64_t(e) * a.N + n0 + c + (kSwiglu && r / 32 % 2 ? half : 0)];
+      } else if (r - BN < nr) {
+        scale[k] = a.row_scale[row0 + r - BN];
+      }
+    }
 
     // Load j of this wave fills rows 8 (j W + wave) .. + 7 of a stage, a lane 16
     // bytes: lane l the slot l % 8 of row l / 8. Slot s of row r holds piece s ^
@@ -367,6 +408,9 @@ __global__ __launch_bounds__(WM * WN * kWave) void product_tile(Int8Args a) {
     for (int s = 0; s < S - 1; ++s)
 #pragma unroll
       for (int j = 0; j < L; ++j) load(j, s, s);
+#pragma unroll
+    for (int k = 0; k < kScales; ++k)
+      if (k * W * kWave + threadIdx.x < BN + BM) scales[k * W * kWave + threadIdx.x] = scale[k];
     // One step's end of the waiting: its loads have come when only those of the
     // later steps are on their way, and the reads of the slot that is filled next
     // are done.
@@ -438,22 +482,18 @@ __global__ __launch_bounds__(WM * WN * kWave) void product_tile(Int8Args a) {
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int c = (wn * NT + h) / (kSwiglu ? 2 : 1) * 32 + 8 * g + 4 * hi;
-        float ws[2][4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float* p = a.w_scale + int64_t(e) * a.N + min(n0 + c + r, limit - 1);
-          ws[0][r] = p[0];
-          ws[1][r] = kSwiglu ? p[half] : 0.0f;
-        }
+        const int at = (wn * NT + h) * 32 + 8 * g + 4 * hi;  // weight row of the tile
+        const f32x4 ws = *reinterpret_cast<const f32x4*>(scales + at);
+        const f32x4 us = *reinterpret_cast<const f32x4*>(scales + (kSwiglu ? at + 32 : at));
 #pragma unroll
         for (int q = 0; q < MT; ++q) {
           const int row = (wm * MT + q) * 32 + (lane & 31);
-          const float xs = a.row_scale[row0 + min(row, nr - 1)];
+          const float xs = scales[BN + row];
           bf16x4 y;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            float v = float(acc[h][q][4 * g + r]) * xs * ws[0][r];
-            if (kSwiglu) v = swiglu(v, float(acc[(h + 1) % NT][q][4 * g + r]) * xs * ws[1][r]);
+            float v = float(acc[h][q][4 * g + r]) * xs * ws[r];
+            if (kSwiglu) v = swiglu(v, float(acc[(h + 1) % NT][q][4 * g + r]) * xs * us[r]);
             y[r] = __bf16(v);
           }
           *reinterpret_cast<bf16x4*>(lds + row * kPitch + c * 2) = y;
