@@ -111,6 +111,16 @@ def test_odd_columns(N, rows):
         check(q, xs, w[0], ws[0], None, out.view(torch.bfloat16))
 
 
+@pytest.mark.parametrize("N", [2050, 2054, 2060, 2064])  # with SwiGLU half as many columns
+@pytest.mark.parametrize("act", [None, "swiglu"])
+@pytest.mark.parametrize("rows", [150, 700, 2100, 4099])
+def test_rows_of_out_at_any_address(rows, act, N):
+    q, xs, w, ws = inputs(rows + N, rows, 1, N, 528)
+    out, err = run(q, xs, w, ws, act)
+    assert err == 0
+    check(q, xs, w[0], ws[0], act, out.view(torch.bfloat16))
+
+
 def check_experts(q, xs, w, ws, act, counts, off, out):
     cap = out.shape[0]
     used = torch.zeros(cap, dtype=torch.bool, device="cuda")
