@@ -88,9 +88,11 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // The first row of expert e in the buffer and how many are in use, without the
-// rows that the buffer does not hold (`over`: there are such).
-__device__ __forceinline__ int run_of(const int32_t* counts, const int32_t* offsets, int64_t cap,
-                                      int e, int64_t* first, bool* over) {
+// rows that the buffer does not hold (`over`: there are such). Ints: a pointer to
+// int32_t, or one for scalar loads.
+template <typename Ints>
+__device__ __forceinline__ int run_of(Ints counts, Ints offsets, int64_t cap, int e,
+                                      int64_t* first, bool* over) {
   const int64_t begin = offsets[e], end = offsets[e + 1];
   const int64_t n = min((int64_t)counts[e], end - begin), held = min(n, cap - begin);
   *first = begin;

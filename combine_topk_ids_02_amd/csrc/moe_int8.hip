@@ -26,6 +26,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef bf16x8 bf16x8_any __attribute__((aligned(2)));  // at any address of a value
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef const __attribute__((address_space(4))) int32_t* scalar_ints;
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kMostRow = 1 << 16;  // values of a row
@@ -54,12 +55,9 @@ template <int BM>
 struct Chunks {
   const Int8Args& a;
   int per, before, mine, total;
+  int run0, first0;  // of this lane's first expert
 
-  __device__ __forceinline__ int count(int e, bool flag) const {
-    int64_t first;
-    bool over;
-    const int run = run_of(a.counts, a.offsets, a.cap, e, &first, &over);
-    if (flag && over) flag_error(a.err, MOE_ERRBIT_EXPERT_CAP);
+  __device__ __forceinline__ static int chunks_of(int run) {
     return run / BM + (run % BM > 0 ? 1 : 0);
   }
 
@@ -71,9 +69,15 @@ struct Chunks {
     }
     const int lane = lane_id();
     per = (a.E + kWave - 1) / kWave;
-    mine = 0;
-    for (int j = 0; j < per; ++j)
-      if (lane * per + j < a.E) mine += count(lane * per + j, flag);
+    mine = run0 = first0 = 0;
+    for (int j = 0; j < per && lane * per + j < a.E; ++j) {
+      int64_t first;
+      bool over;
+      const int run = run_of(a.counts, a.offsets, a.cap, lane * per + j, &first, &over);
+      if (flag && over) flag_error(a.err, MOE_ERRBIT_EXPERT_CAP);
+      mine += chunks_of(run);
+      if (j == 0) run0 = run, first0 = int(first);  // offsets are int32
+    }
     int upto = mine;
     for (int s = 1; s < kWave; s <<= 1) {
       const int up = __shfl_up(upto, s);
@@ -83,6 +87,13 @@ struct Chunks {
     total = read_lane(upto, kWave - 1);
   }
 
+  // Tiles, with those of the columns. Weights and rows of out that this card's memory
+  // holds make fewer than 2^31; counts of no layout may not: they get none.
+  __device__ __forceinline__ uint32_t all() const {
+    const int64_t n = int64_t(total) * a.tiles;
+    return n > 0 && n < int64_t(1) << 31 ? uint32_t(n) : 0;
+  }
+
   // Tile i of the total * tiles that the chunks make with the column tiles: its
   // expert, column tile, first row and number of rows. Workgroups go round the 8 XCDs
   // one by one, so each XCD is given a contiguous eighth of an order that goes through
@@ -90,13 +101,11 @@ struct Chunks {
   // time shares rows and weights in its L2, and weights are wanted only once. (With
   // 8 chunks of whatever experts at a time 8,192 rows of 32 experts, K = 2,048, N = 7,168,
   // read 690 MB for 490 and took 205 us instead of 196; 1,536 rows of 48, 110 and 106.)
-  // T: 32 bits, where they do. False where there is no such tile (counts of no
-  // layout, whose sum has overflowed).
-  template <typename T>
-  __device__ __forceinline__ bool tile(T i, int* expert, int* col, int64_t* row0,
+  // False where there is no such tile (counts of no layout, whose sum has overflowed).
+  __device__ __forceinline__ bool tile(uint32_t i, int* expert, int* col, int64_t* row0,
                                        int* rows) const {
-    const T tiles = a.tiles, all = T(total) * tiles, x = i % 8;
-    T at = x * (all / 8) + min(x, T(all % 8)) + i / 8;
+    const uint32_t tiles = a.tiles, all = this->all(), x = i % 8;
+    uint32_t at = x * (all / 8) + min(x, all % 8) + i / 8;
     int e = 0, run = a.dense, n = total;
     int64_t first = 0;
     if (a.counts) {
@@ -104,33 +113,28 @@ struct Chunks {
       const uint64_t hit = __ballot(v >= before && v < before + mine);
       if (!hit) return false;
       const int l = __ffsll((unsigned long long)hit) - 1;
-      at -= T(read_lane(before, l)) * tiles;
-      int j = 0;
-      for (;; ++j) {
-        e = l * per + j;
-        if (j == per || e >= a.E) return false;
-        bool over;
-        run = __builtin_amdgcn_readfirstlane(run_of(a.counts, a.offsets, a.cap, e, &first, &over));
-        n = run / BM + (run % BM > 0 ? 1 : 0);
-        if (at < T(n) * tiles) break;
-        at -= T(n) * tiles;
+      at -= uint32_t(read_lane(before, l)) * tiles;
+      e = l * per;
+      run = read_lane(run0, l);
+      first = read_lane(first0, l);
+      n = chunks_of(run);
+      for (int j = 1; at >= n * tiles; ++j) {
+        at -= n * tiles;
+        if (j == per || ++e == a.E) return false;
+        bool over;  // scalar loads: the kernel does not write what they read
+        run = run_of(scalar_ints(uint64_t(a.counts)), scalar_ints(uint64_t(a.offsets)), a.cap, e,
+                     &first, &over);
+        n = chunks_of(run);
       }
-      first = __builtin_amdgcn_readfirstlane(int(first));  // offsets are int32
     }
-    const T g = at / (8 * tiles), rest = at - g * 8 * tiles;
-    const T held = min(T(8), T(n - int(g) * 8));
-    const int chunk = int(g) * 8 + int(rest % held);
+    const uint32_t g = at / (8 * tiles), rest = at - g * 8 * tiles;
+    const uint32_t held = min(8u, n - g * 8);
+    const int chunk = g * 8 + rest % held;
     *expert = e;
     *col = int(rest / held);
     *row0 = first + int64_t(chunk) * BM;
     *rows = min(BM, run - chunk * BM);
     return true;
-  }
-
-  __device__ __forceinline__ bool tile(int64_t i, int64_t all, int* expert, int* col,
-                                       int64_t* row0, int* rows) const {
-    return all < int64_t(1) << 28 ? tile<uint32_t>(uint32_t(i), expert, col, row0, rows)
-                                  : tile<int64_t>(i, expert, col, row0, rows);
   }
 };
 
@@ -173,11 +177,11 @@ __global__ __launch_bounds__(W * kWave) void product_few(Int8Args a) {
   const int each = (granules + W - 1) / W;
   const int g0 = wave * each, steps = max(0, min(each, granules - g0));
   const Chunks<BM> chunks(a, blockIdx.x == 0 && wave == 0);
-  const int64_t all = int64_t(chunks.total) * a.tiles;
-  for (int64_t i = blockIdx.x; i < all; i += gridDim.x) {
+  const uint32_t all = chunks.all();
+  for (uint32_t i = blockIdx.x; i < all; i += gridDim.x) {
     int col, e, nr;
     int64_t row0;
-    if (!chunks.tile(i, all, &e, &col, &row0, &nr)) return;
+    if (!chunks.tile(i, &e, &col, &row0, &nr)) return;
     const int n0 = col * kCols;
     const int8_t* w0 = a.w + (int64_t(e) * a.N + n0) * a.K;
     buffer wb[NT];
@@ -330,11 +334,11 @@ __global__ __launch_bounds__(WM * WN * kWave) void product_tile(Int8Args a) {
   const int half = a.N / 2, limit = kSwiglu ? half : a.N;
   const int steps = (a.K + kGranule - 1) / kGranule;
   const Chunks<BM> chunks(a, blockIdx.x == 0 && wave == 0);
-  const int64_t all = int64_t(chunks.total) * a.tiles;
-  for (int64_t i = blockIdx.x; i < all; i += gridDim.x) {
+  const uint32_t all = chunks.all();
+  for (uint32_t i = blockIdx.x; i < all; i += gridDim.x) {
     int col, e, nr;
     int64_t row0;
-    if (!chunks.tile(i, all, &e, &col, &row0, &nr)) return;
+    if (!chunks.tile(i, &e, &col, &row0, &nr)) return;
     const int n0 = col * kCols, held = min(kCols, limit - n0);
     const int8_t* w0 = a.w + (int64_t(e) * a.N + n0) * a.K;
     const buffer wg = make_buffer(w0, held * a.K);
@@ -617,7 +621,12 @@ int moe_int8_product(const moe_shape_t* shape, int N, int act, const int8_t* row
   const int64_t tiles = column_tiles(kForms[form], N);
   const Int8Args a{rows, row_scale, expert_counts, expert_offsets, w_q, w_scale, out, err_word,
                    cap_expert, int(pairs), shape->E, shape->H, N, swiglu ? N / 2 : N, int(tiles)};
-  const dim3 grid(uint32_t(std::min<int64_t>(chunks * tiles, kMostGroups)));
+  // The two large tiles go round the workgroups that the CUs hold at once, which find
+  // the experts' chunks only once (8,192 rows of 32 experts, K = 2,048, N = 7,168 185 us
+  // against 197); smaller ones are taken as CUs come free (384 rows of 48 experts, K =
+  // 5,120, N = 4,096 169 us against 171).
+  const bool large = kForms[form].waves == 8 && kForms[form].over_k == 1;
+  const dim3 grid(uint32_t(std::min<int64_t>(chunks * tiles, large ? 256 : kMostGroups)));
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (swiglu)
     launch<true>(form, grid, st, a);
