@@ -189,6 +189,16 @@ def test_counts_of_no_layout(T):
         run(q, xs, w, ws, None, counts, off, T, 1)
 
 
+@pytest.mark.parametrize("T", [10, 300, 3000])
+def test_counts_of_no_layout_of_many_experts(T):
+    """More experts than a wave has lanes, all of them with the whole buffer."""
+    E, big = 130, 2 ** 31 - 1
+    q, xs, w, ws = inputs(8, 64, E, 32, 64)
+    for counts, off in [([big] * E, [0] + [big] * E), ([64] * E, [-1] * (E + 1)),
+                        ([1, -1] * (E // 2), list(range(E + 1)))]:
+        run(q, xs, w, ws, None, counts, off, T, 1)
+
+
 def test_numbers_of_rows_that_the_binding_is_given():
     """Without T all rows, whatever k; with T the first T * k."""
     q, xs, w, ws = inputs(12, 7, 1, 32, 64)
