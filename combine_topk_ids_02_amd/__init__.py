@@ -76,14 +76,28 @@ class MoeError(RuntimeError):
 
 
 _lib = None
-_address = None if _fast is None else _fast.address
-# its functions, in the order of its bind()
+_address = None  # the C++ module's, once lib() has found that it fits
+# its functions, in the order of its bind() and built_for()
 _FAST_CALLS = ("moe_norm", "moe_norm_backward", "moe_quantise_rows", "moe_int8_product")
+
+
+# arguments' types as the C++ module's built_for() names them
+_KINDS = {ctypes.c_void_p: "p", ctypes.POINTER(MoeShape): "p", ctypes.c_int: "i",
+          ctypes.c_int64: "q", ctypes.c_size_t: "n", ctypes.c_float: "f"}
+
+
+def _fits(module, L) -> bool:
+    """Whether the C++ module was compiled for this torch, this version of the library
+    and the signatures declared here."""
+    want = (ABI_VERSION, str(torch.__version__),
+            *("".join(_KINDS.get(t, "?") for t in getattr(L, name).argtypes)
+              for name in _FAST_CALLS))
+    return hasattr(module, "built_for") and module.built_for() == want
 
 
 def lib():
     """Load the library (once) and declare its signatures."""
-    global _lib
+    global _lib, _fast, _address
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -171,9 +185,12 @@ def lib():
     if L.moe_abi_version() != ABI_VERSION:
         raise MoeError(f"{LIB_PATH} has ABI version {L.moe_abi_version()}, this binding "
                        f"expects {ABI_VERSION}: rebuild with __graft_entry__.build()")
-    if _fast is not None:
+    if _fast is not None and _fits(_fast, L):
         _fast.bind(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value
                      for name in _FAST_CALLS))
+        _address = _fast.address
+    else:
+        _fast = _address = None
     _lib = L
     return L
 

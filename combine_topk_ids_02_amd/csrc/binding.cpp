@@ -3,7 +3,8 @@
 // norm with 8 tensors took 9 us on the host through ctypes alone; its kernel takes
 // 3.4 us. Nothing is kept between calls, and nothing is decided here: a tensor that
 // is not what a call needs gives None, and the Python code then says what is wrong
-// with it. The package works without this module, only slower.
+// with it. The package works without this module, only slower; it is used only
+// where built_for() is what the library and torch are.
 
 #include <Python.h>
 #include <torch/csrc/Dtype.h>
@@ -13,6 +14,10 @@
 #include <utility>
 
 #include "moe_dispatch.h"
+
+#ifndef MOE_BUILT_FOR_TORCH
+#error "the torch this is compiled against, as a string (torch.__version__)"
+#endif
 
 namespace {
 
@@ -44,11 +49,13 @@ PyObject* address(PyObject*, PyObject* const* args, Py_ssize_t n) {
 }
 
 // An argument of a library call from its Python object: an address (None: NULL) or
-// a structure, or a number. `ok` turns false where it is neither.
+// a structure, or a number. `ok` turns false where it is neither. `kind` stands for
+// the type in built_for().
 template <typename T>
 struct Arg;
 template <typename T>
 struct Arg<T*> {
+  static constexpr char kind = 'p';
   static T* from(PyObject* o, bool& ok) {
     if (o == Py_None) return nullptr;
     if (PyLong_Check(o)) {
@@ -74,18 +81,22 @@ T whole(PyObject* o, bool& ok) {
 }
 template <>
 struct Arg<int> {
+  static constexpr char kind = 'i';
   static int from(PyObject* o, bool& ok) { return whole<int>(o, ok); }
 };
 template <>
 struct Arg<int64_t> {
+  static constexpr char kind = 'q';
   static int64_t from(PyObject* o, bool& ok) { return whole<int64_t>(o, ok); }
 };
 template <>
 struct Arg<size_t> {
+  static constexpr char kind = 'n';
   static size_t from(PyObject* o, bool& ok) { return whole<size_t>(o, ok); }
 };
 template <>
 struct Arg<float> {
+  static constexpr char kind = 'f';
   static float from(PyObject* o, bool& ok) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) ok = false;
@@ -100,6 +111,7 @@ struct Entry;
 template <typename... A, int (*Declared)(A...)>
 struct Entry<Declared> {
   static inline int (*at)(A...) = nullptr;
+  static constexpr char kinds[] = {Arg<A>::kind..., 0};
 
   template <size_t... I>
   static int run(PyObject* const* args, bool& ok, std::index_sequence<I...>) {
@@ -132,6 +144,15 @@ struct Entry<Declared> {
   }
 };
 
+// built_for(): the library's version, torch's, and the kinds of the arguments of each
+// function below that this module was compiled for. A file that an earlier build left
+// would pass arguments on in an order or width that the library no longer takes.
+PyObject* built_for(PyObject*, PyObject*) {
+  return Py_BuildValue("(isssss)", MOE_DISPATCH_ABI_VERSION, MOE_BUILT_FOR_TORCH,
+                       Entry<&moe_norm>::kinds, Entry<&moe_norm_backward>::kinds,
+                       Entry<&moe_quantise_rows>::kinds, Entry<&moe_int8_product>::kinds);
+}
+
 // bind(address of each function below, in this order)
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != 4 || !Entry<&moe_norm>::bind(args[0]) || !Entry<&moe_norm_backward>::bind(args[1]) ||
@@ -144,6 +165,7 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 #define FAST(name, f) {name, reinterpret_cast<PyCFunction>(f), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {FAST("address", address),
+                          {"built_for", built_for, METH_NOARGS, nullptr},
                           FAST("bind", bind),
                           FAST("moe_norm", Entry<&moe_norm>::call),
                           FAST("moe_norm_backward", Entry<&moe_norm_backward>::call),
