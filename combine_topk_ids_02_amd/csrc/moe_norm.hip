@@ -364,15 +364,33 @@ struct NormGradArgs {
   int waves, at_once;  // waves a row, rows a workgroup
 };
 
+// Rows that a thread adds up in one float32 value, at most.
+constexpr int kShortSum = 16;
+
 // With g = d_out * w and unit = h * inv: d_h = inv * (g - unit * mean(g * unit))
 // + d_sum. A workgroup takes `at_once` rows at a time, W waves each, and keeps the
 // sums of d_out * unit in registers; at the end its rows' meet in LDS, one after
 // the other, and norm_grad_join adds up the workgroups' in a fixed order.
-template <bool kF32, bool kWeightF32, int NC>
-__global__ __launch_bounds__(kMostWaves * kWave) void norm_grad(NormGradArgs a) {
+//
+// kLong: a thread adds up more than kShortSum rows, and one float32 sum's error would
+// grow with them (2^23 rows of 8 equal values, 1,024 a thread: 1e-5 of the sum). So
+// after every kShortSum rows the sums in registers are added to two float32 values each,
+// what the addition to the one rounds off going to the other. These lie in LDS as long
+// as two workgroups of a CU have room for both (up to 8 sums a thread); else the first
+// has the workgroup's row of `part`. It costs 1% up to 8,192 values a row and 2 to 8%
+// beyond (16,384 rows of 10,240 in bf16 256 us, one sum 247; with the second values
+// brought up to date at every row, in LDS, 310). With 16 sums a thread in bf16 the
+// registers are held to 80, as without kLong: two workgroups of up to 12 waves a CU
+// (82 registers: 292 us).
+template <bool kF32, bool kWeightF32, int NC, bool kLong>
+__global__ __launch_bounds__(kMostWaves * kWave)
+__attribute__((amdgpu_waves_per_eu(kLong && !kF32 && NC == 2 ? 6 : 4))) void norm_grad(
+    NormGradArgs a) {
   constexpr int N = kPieceOf<kF32>;
+  constexpr int kSums = NC * kMostWaves * kWave * N;  // of a workgroup
+  constexpr bool kFirstInLds = NC * N <= 8;
   __shared__ float part[2][kMostWaves];
-  __shared__ __align__(16) float joined[NC * kMostWaves / 2 * kWave * N];
+  __shared__ __align__(16) float joined[kLong ? (kFirstInLds ? 2 : 1) * kSums : kSums / 2];
   const int W = a.waves, threads = W * kWave;
   const int mine = wave_in_block() / W, wave = wave_in_block() % W;  // its row of those at once
   const int thread = wave * kWave + lane_id();
@@ -389,11 +407,54 @@ __global__ __launch_bounds__(kMostWaves * kWave) void norm_grad(NormGradArgs a) 
 #pragma unroll
     for (int j = 0; j < N; ++j) dw[i].v[j] = 0.0f;
   }
+  // Adds the sums to their two parts, which are 0 before the `begin`ning, or at the
+  // `end` makes them of both. In LDS 4 neighbouring sums of all threads lie next to each
+  // other; in `part` (at_once is 1 then) the sums lie as they do at the end.
+  int rows = 0;
+  auto empty = [&](bool begin, bool end) {
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));  // no addresses of this kept in registers over the rows
+    f32x4* low = reinterpret_cast<f32x4*>(joined) + t;
+    f32x4* first = low + kSums / 4;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int p = i * threads + (kFirstInLds ? thread : t);
+      if (p < pieces) {
+        if (!kFirstInLds)
+          first = reinterpret_cast<f32x4*>(a.part) + (int64_t(blockIdx.x) * pieces + p) * (N / 4);
+#pragma unroll
+        for (int k = 0; k < N / 4; ++k) {
+          f32x4& one_at = first[kFirstInLds ? (i * (N / 4) + k) * blockDim.x : k];
+          f32x4& two_at = low[(i * (N / 4) + k) * blockDim.x];
+          f32x4 one = {0, 0, 0, 0}, two = {0, 0, 0, 0};
+          if (!begin) one = one_at, two = two_at;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float& sum = dw[i].v[4 * k + j];
+            const float add = end && rows % kShortSum == 0 ? 0.0f : sum;
+            const float now = one[j] + add, step = now - one[j];
+            two[j] += (one[j] - (now - step)) + (add - step);
+            one[j] = now;
+            const float both = now + two[j];  // (none where a sum is not finite)
+            if (end) sum = fabsf(both) < __builtin_inff() ? both : now;
+          }
+          if (!end) one_at = one, two_at = two;
+        }
+      }
+    }
+  };
   int turn = 0;
   for (int row0 = blockIdx.x * a.at_once; row0 < a.T; row0 += gridDim.x * a.at_once, turn ^= 1) {
     const int row = row0 + mine;
     const bool live = row < a.T;
     const int64_t at0 = int64_t(row) * pieces;
+    if (kLong) {  // (not where they are added to their parts: it took 3 more registers)
+      const bool anew = rows % kShortSum == 0;
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int j = 0; j < N; ++j) dw[i].v[j] = anew ? 0.0f : dw[i].v[j];
+    }
     Piece<false, N> d[NC];
     Piece<kF32, N> h[NC], through[NC];
 #pragma unroll
@@ -439,8 +500,13 @@ __global__ __launch_bounds__(kMostWaves * kWave) void norm_grad(NormGradArgs a) 
         if (a.d_x) store_piece<false, true>(a.d_x, at0 + p, r);
       }
     }
+    if (kLong && ++rows % kShortSum == 0) empty(rows == kShortSum, false);
   }
   if (!a.part) return;
+  if (kLong) {
+    empty(rows < kShortSum, true);
+    __syncthreads();  // the parts make room for the rows' sums
+  }
   for (int r = 1; r < a.at_once; ++r) {  // (at_once > 1: at most half the waves a row)
     if (mine == r) {
 #pragma unroll
@@ -584,15 +650,24 @@ void launch_norm(int fmt, int each, dim3 grid, int threads, hipStream_t st, cons
     launch_norm<kF32, kWeightF32, kNone>(each, grid, threads, st, a);
 }
 
-template <bool kF32, bool kWeightF32>
+template <bool kF32, bool kWeightF32, bool kLong>
 void launch_grad(int each, dim3 grid, int threads, hipStream_t st, const NormGradArgs& a) {
   switch (each) {
-    case 1: norm_grad<kF32, kWeightF32, 1><<<grid, threads, 0, st>>>(a); break;
-    case 2: norm_grad<kF32, kWeightF32, 2><<<grid, threads, 0, st>>>(a); break;
-    case 4: norm_grad<kF32, kWeightF32, 4><<<grid, threads, 0, st>>>(a); break;
+    case 1: norm_grad<kF32, kWeightF32, 1, kLong><<<grid, threads, 0, st>>>(a); break;
+    case 2: norm_grad<kF32, kWeightF32, 2, kLong><<<grid, threads, 0, st>>>(a); break;
+    case 4: norm_grad<kF32, kWeightF32, 4, kLong><<<grid, threads, 0, st>>>(a); break;
     default:  // only a float32 stream has as many pieces
-      norm_grad<kF32, kWeightF32, kF32 ? 8 : 4><<<grid, threads, 0, st>>>(a);
+      norm_grad<kF32, kWeightF32, kF32 ? 8 : 4, kLong><<<grid, threads, 0, st>>>(a);
   }
+}
+
+template <bool kF32, bool kWeightF32>
+void launch_grad(bool is_long, int each, dim3 grid, int threads, hipStream_t st,
+                 const NormGradArgs& a) {
+  if (is_long)
+    launch_grad<kF32, kWeightF32, true>(each, grid, threads, st, a);
+  else
+    launch_grad<kF32, kWeightF32, false>(each, grid, threads, st, a);
 }
 
 template <bool kWide>
@@ -701,16 +776,18 @@ int moe_norm_backward(const moe_shape_t* shape, int stream_type, const uint16_t*
     const NormGradArgs a{d_out,      sum,  weight,   d_sum,    inv_rms, d_x,
                          d_residual, part, shape->T, shape->H, waves,   at_once};
     const dim3 grid(groups);
+    // (at_once is 1 then where a lane has more than 8 sums: rows of 9 waves and more)
+    const bool is_long = d_weight && shape->T > int64_t(kShortSum) * groups * at_once;
     if (f32) {
       if (weight_type == MOE_TYPE_F32)
-        launch_grad<true, true>(each, grid, threads, st, a);
+        launch_grad<true, true>(is_long, each, grid, threads, st, a);
       else
-        launch_grad<true, false>(each, grid, threads, st, a);
+        launch_grad<true, false>(is_long, each, grid, threads, st, a);
     } else {
       if (weight_type == MOE_TYPE_F32)
-        launch_grad<false, true>(each, grid, threads, st, a);
+        launch_grad<false, true>(is_long, each, grid, threads, st, a);
       else
-        launch_grad<false, false>(each, grid, threads, st, a);
+        launch_grad<false, false>(is_long, each, grid, threads, st, a);
     }
     const int status = launch_status();
     if (status != MOE_OK || !d_weight) return status;
