@@ -4,15 +4,18 @@
 // All three are one pass over their rows: a row lies in the registers of W
 // waves (pieces of 4 or 8 values, NC of them a lane), is read once in loads that are
 // all on their way before the first is used, and its sum or maximum is joined
-// through DPP and, with W > 1, 64 bytes of LDS. What bounds them is the memory:
-// few operations a value. Measured (kernel time, three sets of buffers in turn):
-//  - norm, 4,093 x 5,120 in bf16 to bf16 and MXFP8 (189 MB) 29.5 us, 6.4 TB/s; 8,192 x
-//    7,168 with a float32 stream (705 MB) 123 us, 5.7 TB/s; one row of 5,120 3.4 us;
-//  - its gradient, 8,192 x 7,168 with a float32 stream (940 MB) 179 us, 5.2 TB/s (512
-//    workgroups of 14 waves; 256 173 us, but 8,192 x 5,120 in bf16 82 instead of 70;
-//    a row's loads before the row ahead is done: 185);
-//  - rows to int8, 24,576 of 2,048 (151 MB) 29.5 us, 5.1 TB/s.
-// A copy of 1 GiB on this card takes its bytes at 5.1 TB/s.
+// through DPP and, with W > 1, a value of each wave in LDS. What bounds them is the
+// memory: few operations a value. Measured (median kernel time of a trace, two sets of
+// buffers in turn):
+//  - norm, 4,093 x 5,120 in bf16 to bf16 and MXFP8 (189 MB, in part from the cache of
+//    256 MB) 28.3 us, 6.7 TB/s; 8,192 x 7,168 with a float32 stream (705 MB) 126 us, 5.6
+//    TB/s; one row of 5,120 2.6 us;
+//  - its gradient, 8,192 x 7,168 with a float32 stream (940 MB) 170 us and 5 for the
+//    weight's sums, 5.4 TB/s (512 workgroups of 14 waves. Calls in a graph: 179 us, with
+//    256 workgroups 173, but 8,192 x 5,120 in bf16 82 instead of 70; a row's loads
+//    before the row ahead is done: 185);
+//  - rows to int8, 24,576 of 2,048 (151 MB) 25.7 us, 5.9 TB/s.
+// A copy of 1 GiB on this card takes its bytes at 5.1 TB/s, a large read at 6.4.
 
 #include "moe_common.h"
 
@@ -692,7 +695,10 @@ bool norm_shape_ok(const moe_shape_t* s, int stream_type, int weight_type) {
          (weight_type == MOE_TYPE_F32 || weight_type == MOE_TYPE_BF16);
 }
 
-// Workgroups of the gradient, at most: two for each CU, all resident at once.
+// Workgroups of the gradient, at most: two for each CU. All are resident at once where a
+// row has at most 8,192 values; the registers of longer ones leave a CU 24 waves (16 sums a
+// thread in bf16), 20 or 16 (in float32) or 16 (32 sums), so that of workgroups of up to 16
+// waves it may hold only one at a time.
 constexpr int kGradGroups = 512;
 
 }  // namespace
