@@ -90,3 +90,34 @@ def test_weight_gradient_that_is_not_finite(stream):
     assert bool(torch.isnan(got[3]))
     assert float(got[4]) == float("inf") and float(got[5]) == float("-inf")
     assert bool((got[[0] + list(range(6, H))] == T).all())
+
+
+@pytest.mark.parametrize("T, H, stream", [(9001, 5120, F32), (9001, 10240, BF), (140000, 64, BF)])
+def test_many_rows_in_a_graph(T, H, stream):
+    """Replayed on a workspace of NaNs, with eager calls between: the same to the bit."""
+    print(f"[graph] {T} x {H} {stream}", flush=True)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    d = torch.randn(T, H, dtype=BF, device="cuda", generator=g)
+    h = torch.randn(T, H, dtype=stream, device="cuda", generator=g)
+    inv, ones = 0.5 + torch.rand(T, device="cuda", generator=g), torch.ones(H, device="cuda")
+    got = torch.empty(H, device="cuda")
+    room = torch.empty(moe.norm_workspace_bytes(T, H) // 4, device="cuda")
+
+    def step():
+        moe.norm_backward(d, h, inv, ones, d_weight=got, workspace=room)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step()
+    for n in range(4):
+        d.mul_(-1)
+        want = weight_gradient(d, h, inv)
+        got.zero_()
+        room.fill_(float("nan"))
+        graph.replay()
+        if n % 2:
+            torch.cuda.synchronize()
+        assert torch.equal(got, want), n
